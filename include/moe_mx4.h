@@ -24,6 +24,14 @@
  *                   while gate_up is still running)
  *   mx4_moe_decode_persistent_static  the same with a library-held workspace (no allocation)
  *
+ * with 8-bit integer weights and activations (a scale per channel and per row), dense and routed:
+ *
+ *   i8_quantize     bf16 / f16 / f32 rows -> 8-bit rows with a scale each
+ *   i8_pack_experts one-time repack of 8-bit weights into the GPU's tiled layout
+ *   i8_gemm         dense product of 8-bit rows with one matrix;  i8_linear: from plain rows
+ *   i8_moe_gemm     the routed experts' projection of mx4_moe_gemm in this format
+ *   i8_moe_decode   the whole layer of a few tokens in two launches
+ *
  * Sources (web pages on the daScript repository's dasLLAMA engine; cited by tag below):
  *   [fusion]  PR #3579 "dasLLAMA gpt-oss arc", commit log, the Metal fusion-lane commit: the
  *             bucket pass computes each expert's padded-prefix base inside its workgroup and
@@ -403,6 +411,124 @@ int mx4_moe_decode_persistent_static(const float* logits, const uint16_t* x, int
                                      int32_t* counts, int32_t* basep, int32_t* row_tok,
                                      int32_t* pos, uint16_t* h, float* d, float* y,
                                      int max_workgroups, void* stream);
+
+/*
+ * 8-bit integer projections (W8A8): whole-number weights with one f32 scale per output channel,
+ * activations quantized per row (per token) to whole numbers with one f32 scale each. The pages
+ * keep 8-bit activations to the CPU; this format on the GPU is outside them.
+ *
+ * Quantized rows: row r of K values has its codes (int8, in [-127, 127]) at q + r*KP, KP =
+ * roundup(K, 64), the KP - K padding codes 0, and its scale at s[r]; value i stands for
+ * q[i] * s[r].
+ */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+#define MOE_I8_MAX_K 65536 /* reduction length: 128 * 128 * K stays inside the exact 32-bit sums */
+
+/*
+ * A stack of E matrices of N rows (output channels) by K columns: W[e][n][i] = q * s[e][n].
+ * q is in the TILED layout that i8_pack_experts writes, s f32 [E][N], bias f32 [E][N] or NULL.
+ * glu = 1: the N = 2F rows are the F gate rows, then the F up rows of a SwiGLU projection, and
+ * each half is tiled on its own; glu = 0 otherwise. The descriptor is a HOST struct.
+ *
+ * Tiled layout: an expert's matrix is cut into tiles of 16 rows by 64 columns (1 KB), zeros past
+ * N (past F in each half when glu) and K. With NT = roundup(N, 16)/16 (glu: 2 * roundup(F, 16)/16)
+ * tiles of rows and C = KP/64 chunks of columns, tile (c, t) of expert e starts at byte
+ * 1024 * ((e*C + c)*NT + t); its byte 256*p + 16*r + i is column 64c + 16p + i of row r, which is
+ * the lane order of the MFMA operand, so a wavefront reads a tile as one contiguous run.
+ */
+typedef struct {
+  const int8_t* q;
+  const float* s;
+  const float* bias;
+  int E;
+  int N;
+  int K;
+  int glu;
+} i8_experts;
+
+/* Bytes of the tiled layout, or -1 for E, N or K < 1, K > MOE_I8_MAX_K, or odd N with glu.
+ * Host-only. */
+int64_t i8_packed_bytes(int E, int N, int K, int glu);
+
+/*
+ * Repack a stack from row-major int8 [E][N][K] to the tiled layout (i8_packed_bytes bytes), once
+ * when the weights are loaded. The buffers must not overlap.
+ * Errors: MOE_EINVAL for NULL pointers or E, N, K < 1; MOE_ESHAPE for E > MOE_MAX_E,
+ *         K > MOE_I8_MAX_K or odd N with glu; MOE_EALIGN for q_dst not 16-byte aligned;
+ *         MOE_ELAUNCH.
+ */
+int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu, int8_t* q_dst,
+                    void* stream);
+
+/*
+ * Quantized rows of x: with m = max_i |x[r][i]|, s[r] = m / 127 (rounded to f32) and
+ * q[r][i] = 127 x[r][i] / m, the exact quotient, rounded half to even. A row of zeros takes
+ * s = 0 and codes 0. A row holding a NaN or an infinity takes s = NaN and codes 0: everything
+ * computed from it is NaN, and no other row is touched.
+ *   x     x_dtype [rows][K], ld elements from one row to the next (ld >= K); any alignment of
+ *         its type is taken, 16-byte aligned rows are read fastest.
+ *   live  i32 [rows] or NULL: rows with live[r] < 0 are skipped (q and s left unwritten).
+ * Errors: MOE_EINVAL for NULL x/q/s, rows or K < 1, unknown x_dtype; MOE_ESHAPE for
+ *         K > MOE_I8_MAX_K, ld < K, rows >= 2^31; MOE_EALIGN for q not 16-byte aligned or x, s
+ *         not aligned to their type; MOE_ELAUNCH.
+ */
+int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live, int64_t rows, int K,
+                int8_t* q, float* s, void* stream);
+
+/*
+ * Dense product of quantized rows with one matrix (w->E == 1):
+ *   out[r][n] = (sum_i aq[r][i] * wq[n][i]) * (as[r] * s[n]) + bias[n]
+ * the sum exact in 32-bit integers, the rest in fp32, rounded once to out_dtype. With glu = 1 the
+ * channels come out in their order (gate rows, then up rows).
+ *   out   out_dtype [rows][N], ld_out elements from one row to the next (ld_out >= N).
+ * i8_linear: the same from plain rows x (as i8_quantize takes them); q_ws (int8 [rows][KP]) and
+ * s_ws (f32 [rows]) are scratch that the call may write and leaves without meaning. Calls that
+ * can run concurrently need distinct scratch.
+ * Errors: MOE_EINVAL for NULL pointers, rows < 1, E/N/K < 1, unknown dtypes, glu not 0 or 1;
+ *         MOE_ESHAPE for E != 1, K > MOE_I8_MAX_K, odd N with glu, a matrix of 2 GB or more,
+ *         ld_out < N, ld < K, rows >= 2^31; MOE_EALIGN for aq (q_ws) or w->q not 16-byte aligned,
+ *         or other pointers not aligned to their type; MOE_ELAUNCH.
+ */
+int i8_gemm(const int8_t* aq, const float* as, int64_t rows, const i8_experts* w, void* out,
+            int out_dtype, int64_t ld_out, void* stream);
+int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows, const i8_experts* w,
+              int8_t* q_ws, float* s_ws, void* out, int out_dtype, int64_t ld_out, void* stream);
+
+/*
+ * Routed-expert projection in this format: arguments, row semantics, epilogue and outputs of
+ * mx4_moe_gemm with activation row x = the quantized row a_row[r] (or r) of (aq, as):
+ *   g[n] = (sum_i aq[i] * wq[e][n][i]) * (as * s[e][n]) + bias[e][n]
+ * MOE_ACT_NONE writes f32 [mpad_max][N], MOE_ACT_SWIGLU_OAI (w->glu == 1) bf16 [mpad_max][N/2].
+ * Rows that are padding or ghost are left unwritten, and so is a live row whose a_row entry is
+ * outside [0, a_rows).
+ * Errors: as mx4_moe_gemm (aq in place of a, also NULL as or w->s), with K <= MOE_I8_MAX_K in
+ *         place of K % 32 == 0; MOE_ESHAPE also for MOE_ACT_SWIGLU_OAI with w->glu == 0 and for
+ *         an expert of 2 GB or more.
+ */
+int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t a_rows,
+                const i8_experts* w, const int32_t* counts, const int32_t* basep, int tile_m,
+                int64_t mpad_max, int act, float alpha, float limit, void* out, void* stream);
+
+/*
+ * The whole layer of a few tokens in two launches ([chain] in this format): what
+ * moe_route_topk, i8_quantize, i8_moe_gemm with MOE_ACT_SWIGLU_OAI, i8_quantize,
+ * i8_moe_gemm with MOE_ACT_NONE and moe_combine compute, bit for bit, with h and d by routed row
+ * rho = t*k + s. An expert is read once however many of the tokens picked it.
+ *   logits f32 [T][E];  x bf16 [T][D];  w_gu: glu = 1, N = 2F, K = D;  w_dn: glu = 0, N = D, K = F
+ *   ids i32 [T][k], w f32 [T][k] out (as moe_route_topk);  h bf16 [T*k][F] out
+ *   d f32 [T*k][D] out or NULL (then never written);  y y_dtype [T][D] out
+ * Errors: MOE_EINVAL for NULL pointers other than d, T, E or k < 1, k > E, unknown y_dtype;
+ *         MOE_ESHAPE for T > MOE_DECODE_MAX_T, k > MOE_DECODE_MAX_K, E > MOE_MAX_E, stacks that do
+ *         not fit each other or E, D or F > MOE_I8_MAX_K, an expert of 2 GB or more, or
+ *         T * D above about 140 000 (the quantized tokens are held in LDS); MOE_EALIGN for x, h,
+ *         w_gu->q or w_dn->q not 16-byte aligned or other pointers not aligned to their type;
+ *         MOE_ELAUNCH.
+ */
+int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, int E, int k,
+                  const i8_experts* w_gu, const i8_experts* w_dn, float alpha, float limit,
+                  int32_t* ids, float* w, uint16_t* h, float* d, void* y, int y_dtype,
+                  void* stream);
 
 /*
  * Router-weighted combine ([chain]: routing-weighted sum of the expert rows in slot order).

@@ -22,7 +22,10 @@ EXPORTS = ("moe_strerror", "moe_mpad_max", "moe_route_topk", "moe_bucket", "mx4_
            "mx4_moe_gemv", "mx4_moe_gemm", "moe_combine", "mx4_moe_decode", "moe_timing_arm",
            "moe_timing_read", "mx8_quantize", "mx4_moe_gemm_mx8", "moe_router",
            "mx4_moe_decode_persistent", "mx4_moe_decode_persistent_static", "moe_probe_read",
-           "moe_probe_mfma_bf16")
+           "moe_probe_mfma_bf16", "i8_packed_bytes", "i8_pack_experts", "i8_quantize", "i8_gemm",
+           "i8_linear", "i8_moe_gemm", "i8_moe_decode")
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_I8_MAX_K = 65536
 MOE_DECODE_WS_WORDS = 544
 MOE_ROUTER_MAX_ROUTED = 16384
 MOE_ROUTER_WS_WORDS = 67584
@@ -38,6 +41,12 @@ class MoeError(RuntimeError):
 class Mx4ExpertsC(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("E", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int)]
+
+
+class I8ExpertsC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("E", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("glu", ctypes.c_int)]
 
 
 _lib = None
@@ -100,6 +109,22 @@ def lib() -> ctypes.CDLL:
         L.moe_probe_read.argtypes = [vp, i64, vp, ci, vp]
         L.moe_probe_mfma_bf16.restype = ci
         L.moe_probe_mfma_bf16.argtypes = [ci, ci, vp, vp]
+        p8 = ctypes.POINTER(I8ExpertsC)
+        L.i8_packed_bytes.restype = i64
+        L.i8_packed_bytes.argtypes = [ci, ci, ci, ci]
+        L.i8_pack_experts.restype = ci
+        L.i8_pack_experts.argtypes = [vp, ci, ci, ci, ci, vp, vp]
+        L.i8_quantize.restype = ci
+        L.i8_quantize.argtypes = [vp, ci, i64, vp, i64, ci, vp, vp, vp]
+        L.i8_gemm.restype = ci
+        L.i8_gemm.argtypes = [vp, vp, i64, p8, vp, ci, i64, vp]
+        L.i8_linear.restype = ci
+        L.i8_linear.argtypes = [vp, ci, i64, i64, p8, vp, vp, vp, ci, i64, vp]
+        L.i8_moe_gemm.restype = ci
+        L.i8_moe_gemm.argtypes = [vp, vp, vp, i64, p8, vp, vp, ci, i64, ci, cf, cf, vp, vp]
+        L.i8_moe_decode.restype = ci
+        L.i8_moe_decode.argtypes = [vp, vp, i64, ci, ci, p8, p8, cf, cf, vp, vp, vp, vp, vp, ci,
+                                    vp]
         _lib = L
     return _lib
 
@@ -443,6 +468,248 @@ def mx4_moe_decode_persistent_static(logits, x, gate_up: MX4Experts, down: MX4Ex
     return out
 
 
+# ---------------------------------------------------------------------------------------------
+# 8-bit integer projections
+# ---------------------------------------------------------------------------------------------
+
+def _i8_dtype(dtype, name: str) -> int:
+    torch = _torch()
+    code = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}.get(dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
+    return code
+
+
+def _same_device(first, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+
+
+def _i8_call(fn: str, device, stream, *args):
+    """The C entry point on `stream` (by default the device's current one), with that device
+    current: a tensor of another device than the current one runs on its own."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        _call(fn, *args, _stream(stream))
+
+
+def _i8_rows(x, name: str, dtype=None) -> int:
+    """Checks a matrix of rows whose elements are contiguous; returns its row pitch (elements)."""
+    if dtype is not None and x.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.device.type != "cuda":
+        raise TypeError(f"{name}: expected a device tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix of rows, got shape {tuple(x.shape)}")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: expected rows of contiguous elements")
+    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        raise ValueError(f"{name}: rows overlap (stride {x.stride(0)} of {x.shape[1]} elements)")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _i8_out(out, shape, dtype, name: str):
+    """Checks an output of the caller's: contiguous, of this shape and type."""
+    _check(out, dtype, name)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+
+
+def i8_pitch(K: int) -> int:
+    """Row pitch in bytes of quantized rows of K values: K padded to a multiple of 64."""
+    return (K + 63) // 64 * 64
+
+
+def i8_row_buffers(rows: int, K: int, device="cuda"):
+    """Buffers for `rows` quantized rows of K values: (q int8 [rows][i8_pitch(K)], s f32 [rows])."""
+    torch = _torch()
+    return (torch.empty((rows, i8_pitch(K)), dtype=torch.int8, device=device),
+            torch.empty(rows, dtype=torch.float32, device=device))
+
+
+class I8Experts:
+    """A device-resident stack of 8-bit integer matrices with a scale per output channel, in the
+    tiled layout that the projections read; a dense projection is a stack of one.
+
+    q int8 [E][N][K] (or [N][K]), s f32 [E][N] (or [N]), bias like s or None. glu: the rows are
+    the gate rows, then the up rows of a SwiGLU projection. Built with one i8_pack_experts call
+    on the current stream; holds its tensors alive."""
+
+    def __init__(self, q, s, bias=None, glu: bool = False, stream=None):
+        torch = _torch()
+        _check(q, torch.int8, "q")
+        _check(s, torch.float32, "s")
+        if q.dim() == 2:
+            q = q.unsqueeze(0)
+        if q.dim() != 3:
+            raise ValueError(f"q: expected shape [E][N][K] or [N][K], got {tuple(q.shape)}")
+        E, N, K = q.shape
+        s = s.reshape(1, -1) if s.dim() == 1 else s
+        if tuple(s.shape) != (E, N):
+            raise ValueError(f"s: expected shape {(E, N)}, got {tuple(s.shape)}")
+        if bias is not None:
+            _check(bias, torch.float32, "bias")
+            bias = bias.reshape(1, -1) if bias.dim() == 1 else bias
+            if tuple(bias.shape) != (E, N):
+                raise ValueError(f"bias: expected shape {(E, N)}, got {tuple(bias.shape)}")
+        _same_device(q, s, bias)
+        glu = int(bool(glu))
+        nbytes = int(lib().i8_packed_bytes(E, N, K, glu))
+        if nbytes < 0:
+            raise MoeError("i8_pack_experts", MOE_ESHAPE)
+        qp = torch.empty(nbytes, dtype=torch.int8, device=q.device)
+        _i8_call("i8_pack_experts", q.device, stream, _ptr(q), E, N, K, glu, _ptr(qp))
+        self.q, self.s, self.bias = qp, s, bias
+        self.E, self.N, self.K, self.glu = E, N, K, glu
+        self.device = q.device
+        self.c = I8ExpertsC(qp.data_ptr(), s.data_ptr(),
+                            None if bias is None else bias.data_ptr(), E, N, K, glu)
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def quantized(cls, w, bias=None, glu: bool = False, stream=None):
+        """The stack of bf16 / f16 / f32 weights w [E][N][K] (or [N][K]): every output channel is
+        quantized as i8_quantize does a row."""
+        N, K = w.shape[-2], w.shape[-1]
+        q, s = i8_quantize(w.reshape(-1, K), stream=stream)
+        q = q[:, :K].contiguous().reshape(-1, N, K)
+        return cls(q, s.reshape(-1, N), bias, glu, stream)
+
+    @property
+    def nbytes(self) -> int:
+        return self.q.numel() + 4 * self.s.numel()
+
+
+def i8_quantize(x, live=None, out=None, stream=None):
+    """Quantized rows of bf16 / f16 / f32 rows x [rows][K] (any row stride): (q int8
+    [rows][i8_pitch(K)], s f32 [rows]). Rows with live[r] < 0 are left unwritten."""
+    torch = _torch()
+    ld = _i8_rows(x, "x")
+    code = _i8_dtype(x.dtype, "x")
+    rows, K = x.shape
+    if live is not None:
+        _i8_out(live, (rows,), torch.int32, "live")
+    if out is None:
+        out = i8_row_buffers(rows, K, x.device)
+    else:
+        _i8_out(out[0], (rows, i8_pitch(K)), torch.int8, "q")
+        _i8_out(out[1], (rows,), torch.float32, "s")
+    q, s = out
+    _same_device(x, live, q, s)
+    _i8_call("i8_quantize", x.device, stream, _ptr(x), code, ld, _ptr(live), rows, K, _ptr(q),
+             _ptr(s))
+    return q, s
+
+
+def _i8_dense_out(out, rows: int, w, out_dtype, device):
+    torch = _torch()
+    if out is None:
+        out = torch.empty((rows, w.N), dtype=out_dtype or torch.bfloat16, device=device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+    ld = _i8_rows(out, "out")
+    if tuple(out.shape) != (rows, w.N):
+        raise ValueError(f"out: expected shape {(rows, w.N)}, got {tuple(out.shape)}")
+    return out, _i8_dtype(out.dtype, "out"), ld
+
+
+def i8_gemm(aq, as_, w: I8Experts, out_dtype=None, out=None, stream=None):
+    """Dense product of quantized rows (aq, as_) with the one matrix of w: out [rows][N] in
+    out_dtype (bf16 by default) or in `out` (any row stride)."""
+    torch = _torch()
+    rows = aq.shape[0]
+    _i8_out(aq, (rows, i8_pitch(w.K)), torch.int8, "aq")
+    _i8_out(as_, (rows,), torch.float32, "as")
+    out, code, ld = _i8_dense_out(out, rows, w, out_dtype, aq.device)
+    _same_device(aq, as_, out, w)
+    _i8_call("i8_gemm", aq.device, stream, _ptr(aq), _ptr(as_), rows, w.ref, _ptr(out), code, ld)
+    return out
+
+
+def i8_linear(x, w: I8Experts, out_dtype=None, out=None, ws=None, stream=None):
+    """Dense projection of bf16 / f16 / f32 rows x [rows][K] (any row stride), quantized per row
+    on the way: out [rows][N] in out_dtype (x's by default) or in `out`. ws: scratch of
+    i8_row_buffers(rows, K) (allocated if None); concurrent calls need distinct scratch."""
+    torch = _torch()
+    ld = _i8_rows(x, "x")
+    code = _i8_dtype(x.dtype, "x")
+    rows, K = x.shape
+    if K != w.K:
+        raise ValueError(f"x: expected rows of {w.K} values, got {K}")
+    if ws is None:
+        ws = i8_row_buffers(rows, K, x.device)
+    else:
+        _i8_out(ws[0], (rows, i8_pitch(K)), torch.int8, "ws[0]")
+        _i8_out(ws[1], (rows,), torch.float32, "ws[1]")
+    if out is None and out_dtype is None:
+        out_dtype = x.dtype
+    out, ocode, ldo = _i8_dense_out(out, rows, w, out_dtype, x.device)
+    _same_device(x, ws[0], ws[1], out, w)
+    _i8_call("i8_linear", x.device, stream, _ptr(x), code, ld, rows, w.ref, _ptr(ws[0]),
+             _ptr(ws[1]), _ptr(out), ocode, ldo)
+    return out
+
+
+def i8_moe_gemm(aq, as_, a_row, w: I8Experts, counts, basep, tile_m: int, mpad_max: int,
+                act=MOE_ACT_NONE, alpha: float = 1.702, limit: float = 7.0, out=None,
+                stream=None):
+    """mx4_moe_gemm in 8-bit integers over quantized rows (aq, as_) from i8_quantize: f32
+    [mpad_max][N], or with MOE_ACT_SWIGLU_OAI (w built with glu) bf16 [mpad_max][N/2]."""
+    torch = _torch()
+    rows = aq.shape[0]
+    _i8_out(aq, (rows, i8_pitch(w.K)), torch.int8, "aq")
+    _i8_out(as_, (rows,), torch.float32, "as")
+    if a_row is not None:
+        _i8_out(a_row, (mpad_max,), torch.int32, "a_row")
+    _i8_out(counts, (w.E,), torch.int32, "counts")
+    _i8_out(basep, (w.E + 1,), torch.int32, "basep")
+    swiglu = act == MOE_ACT_SWIGLU_OAI
+    shape = (mpad_max, w.N // 2 if swiglu else w.N)
+    dtype = torch.bfloat16 if swiglu else torch.float32
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=aq.device)
+    else:
+        _i8_out(out, shape, dtype, "out")
+    _same_device(aq, as_, a_row, counts, basep, out, w)
+    _i8_call("i8_moe_gemm", aq.device, stream, _ptr(aq), _ptr(as_), _ptr(a_row), rows, w.ref,
+             _ptr(counts), _ptr(basep), tile_m, mpad_max, act, float(alpha), float(limit),
+             _ptr(out))
+    return out
+
+
+def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha: float = 1.702,
+                  limit: float = 7.0, want_d: bool = False, y_dtype=None, out=None, stream=None):
+    """The whole 8-bit layer of a few tokens (two launches). Returns a dict with ids, w [T][k], h
+    bf16 [T*k][F] and d f32 [T*k][D] in routed-row order (d only with want_d), and y [T][D] in
+    y_dtype (f32 by default). `out` may hold preallocated tensors under those keys."""
+    torch = _torch()
+    _check(logits, torch.float32, "logits")
+    _check(x, torch.bfloat16, "x")
+    if logits.dim() != 2 or tuple(x.shape) != (logits.shape[0], gate_up.K):
+        raise ValueError(f"logits {tuple(logits.shape)}, x {tuple(x.shape)}: expected [T][E] and "
+                         f"[T][{gate_up.K}]")
+    T, E = logits.shape
+    D, F = gate_up.K, gate_up.N // 2
+    o = dict(out or {})
+    if y_dtype is None:
+        y_dtype = o["y"].dtype if "y" in o else torch.float32
+    shapes = {"ids": ((T, k), torch.int32), "w": ((T, k), torch.float32),
+              "h": ((T * k, F), torch.bfloat16), "y": ((T, D), y_dtype)}
+    if want_d or "d" in o:
+        shapes["d"] = ((T * k, D), torch.float32)
+    for key, (shape, dt) in shapes.items():
+        if key in o:
+            _i8_out(o[key], shape, dt, key)
+        else:
+            o[key] = torch.empty(shape, dtype=dt, device=x.device)
+    _same_device(x, logits, gate_up, down, *(o[key] for key in shapes))
+    _i8_call("i8_moe_decode", x.device, stream, _ptr(logits), _ptr(x), T, E, k, gate_up.ref,
+             down.ref, float(alpha), float(limit), _ptr(o["ids"]), _ptr(o["w"]), _ptr(o["h"]),
+             _ptr(o.get("d")), _ptr(o["y"]), _i8_dtype(y_dtype, "y"))
+    return o
+
+
 def moe_timing_arm(n: int) -> None:
     """Time the library's next n kernel launches (kernel execution only); 0 disarms."""
     _call("moe_timing_arm", int(n))
@@ -455,15 +722,18 @@ def moe_timing_read(n: int) -> list:
     return [float(buf[i]) for i in range(n)]
 
 
-def moe_layer(x, logits, gate_up: MX4Experts, down: MX4Experts, k: int, tile_m: int,
+def moe_layer(x, logits, gate_up, down, k: int, tile_m: int,
               alpha: float = 1.702, limit: float = 7.0, projection: str = "gemm", stream=None):
     """One routed-expert MoE layer: route -> bucket -> gate_up+SwiGLU -> down -> combine.
     projection: "gemm" or "gemv" (bf16 activations), or "gemm_mx8" (MXFP8 activations on the
     MX-scaled MFMA: x quantized once, h written as MXFP8 rows by the gate_up epilogue; returns
-    xq/xs/hq/hs and no bf16 h).
+    xq/xs/hq/hs and no bf16 h); these take MX4Experts. "i8" takes I8Experts (gate_up with glu):
+    x and h quantized per row (xq/xs/hq/hs are returned too).
     Returns a dict of every intermediate (device tensors)."""
-    if projection not in ("gemm", "gemv", "gemm_mx8"):
+    if projection not in ("gemm", "gemv", "gemm_mx8", "i8"):
         raise ValueError(f"unknown projection {projection!r}")
+    if (projection == "i8") != (isinstance(gate_up, I8Experts) and isinstance(down, I8Experts)):
+        raise TypeError(f"projection {projection!r} and {type(gate_up).__name__} weights")
     T, E = logits.shape
     ids, w = moe_route_topk(logits, k, stream=stream)
     mpad = moe_mpad_max(T, k, E, tile_m)
@@ -476,6 +746,14 @@ def moe_layer(x, logits, gate_up: MX4Experts, down: MX4Experts, k: int, tile_m: 
         d = mx4_moe_gemm_mx8(hq, hs, None, down, counts, basep, tile_m, mpad, MOE_ACT_NONE,
                              alpha, limit, stream=stream)
         h = None
+        extra = {"xq": xq, "xs": xs, "hq": hq, "hs": hs}
+    elif projection == "i8":
+        xq, xs = i8_quantize(x, stream=stream)
+        h = i8_moe_gemm(xq, xs, row_tok, gate_up, counts, basep, tile_m, mpad,
+                        MOE_ACT_SWIGLU_OAI, alpha, limit, stream=stream)
+        hq, hs = i8_quantize(h, live=row_tok, stream=stream)
+        d = i8_moe_gemm(hq, hs, None, down, counts, basep, tile_m, mpad, MOE_ACT_NONE, alpha,
+                        limit, stream=stream)
         extra = {"xq": xq, "xs": xs, "hq": hq, "hs": hs}
     else:
         fn = mx4_moe_gemm if projection == "gemm" else mx4_moe_gemv

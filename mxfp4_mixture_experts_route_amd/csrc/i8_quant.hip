@@ -1,0 +1,149 @@
+// i8_quantize: rows of bf16, f16 or f32 values -> rows of 8-bit whole numbers with one scale each,
+// the activations of the 8-bit integer projections. i8_pack_experts: the one-time weight repack.
+//
+// The row's largest magnitude m gives the scale m / 127; the codes are 127 x / m rounded half to
+// even, exactly (i8.hpp). The format and the operators on it are not on the pages, which keep
+// activations in 16 bits on the GPU and quantize them to 8-bit blocks on the CPU only.
+//
+// Bound by memory: K * size bytes in, K out, a row read once (it stays in registers between the
+// maximum and the rounding).
+#include "i8.hpp"
+#include "launch.hpp"
+
+namespace moe {
+
+constexpr int kI8QuantThreads = 256;
+
+// TPR threads per row (a wavefront or the whole workgroup), NV vectors of 8 values per thread in
+// registers; what a longer row has past TPR * NV * 8 values is read a second time.
+template <int DT, bool VEC, int TPR, int NV>
+__global__ void __launch_bounds__(kI8QuantThreads)
+i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __restrict__ live,
+                   int64_t rows, int K, int8_t* __restrict__ q, float* __restrict__ s) {
+  const int KP = i8_pitch(K), V = KP >> 3;
+  const int lane = (int)threadIdx.x % TPR;
+  const int64_t r = (int64_t)blockIdx.x * (kI8QuantThreads / TPR) + threadIdx.x / TPR;
+  if (r >= rows || (live && live[r] < 0)) return;   // TPR lanes leave together
+  const int64_t base = r * ld;
+  float v[NV][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int u = lane + i * TPR;
+    if (u < V) {
+      load8<DT, VEC>(x, base + (int64_t)u * 8, K - u * 8, v[i]);
+      m = max_abs8(v[i], m);
+    }
+  }
+  for (int u = lane + NV * TPR; u < V; u += TPR) {
+    float t[8];
+    load8<DT, VEC>(x, base + (int64_t)u * 8, K - u * 8, t);
+    m = max_abs8(t, m);
+  }
+  m = wave_umax(m);
+  if constexpr (TPR > kWave) {
+    __shared__ uint32_t part[TPR / kWave];
+    if ((lane & 63) == 0) part[lane >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < TPR / kWave; ++w) m = max(m, part[w]);
+  }
+  const I8Quant z(m);
+  int8_t* dst = q + r * KP;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int u = lane + i * TPR;
+    if (u < V) *reinterpret_cast<uint2*>(dst + u * 8) = codes8<DT>(z, v[i]);
+  }
+  for (int u = lane + NV * TPR; u < V; u += TPR) {
+    float t[8];
+    load8<DT, VEC>(x, base + (int64_t)u * 8, K - u * 8, t);
+    *reinterpret_cast<uint2*>(dst + u * 8) = codes8<DT>(z, t);
+  }
+  if (lane == 0) s[r] = z.s;
+}
+
+// One lane per 16 bytes of the packed stack: tile t of chunk c holds rows 16 t .. 16 t + 15 and
+// K values 64 c .. 64 c + 63 in the lane order of the MFMA operand (lane l: row l % 16, values
+// 16 (l / 16) ..), zeros past N and K.
+__global__ void __launch_bounds__(256)
+i8_pack_kernel(const int8_t* __restrict__ src, int64_t total, int N, int K, int glu,
+               int8_t* __restrict__ dst) {
+  const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (gid >= total) return;
+  const int NT = i8_tiles(N, glu), C = i8_pitch(K) / kI8Chunk;
+  const int l = (int)(gid & 63);
+  const int64_t tile = gid >> 6;
+  const int t = (int)(tile % NT);
+  const int64_t ec = tile / NT;
+  const int c = (int)(ec % C);
+  const int64_t e = ec / C;
+  const int n = i8_channel(t, l & 15, N, glu);
+  const int k0 = c * kI8Chunk + (l >> 4) * 16;
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (n >= 0) {
+    const int8_t* row = src + (e * N + n) * (int64_t)K;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (k0 + i < K) w[i >> 2] |= (uint32_t)(uint8_t)row[k0 + i] << (8 * (i & 3));
+  }
+  *reinterpret_cast<uint4*>(dst + gid * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT>
+int launch_quantize(const void* x, int64_t ld, const int32_t* live, int64_t rows, int K,
+                    int8_t* q, float* s, hipStream_t st) {
+  constexpr int kSize = DT == MOE_F32 ? 4 : 2;
+  const bool vec = !((uintptr_t)x & 15) && (rows == 1 || (ld * kSize) % 16 == 0);
+  // many rows: a wavefront each (4 a workgroup); few rows, or rows that a wavefront does not
+  // hold in registers: a workgroup each
+  if (K <= kWave * 8 * 8 && rows >= 1024) {
+    const dim3 grid((unsigned)((rows + 3) / 4));
+    if (vec)
+      launch(i8_quantize_kernel<DT, true, 64, 8>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
+    else
+      launch(i8_quantize_kernel<DT, false, 64, 8>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
+  } else {
+    const dim3 grid((unsigned)rows);
+    if (vec)
+      launch(i8_quantize_kernel<DT, true, 256, 4>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
+    else
+      launch(i8_quantize_kernel<DT, false, 256, 4>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
+}
+
+}  // namespace moe
+
+extern "C" int64_t i8_packed_bytes(int E, int N, int K, int glu) {
+  if (E < 1 || N < 1 || K < 1 || K > MOE_I8_MAX_K || (glu != 0 && (N & 1))) return -1;
+  return (int64_t)E * moe::i8_tiles(N, glu != 0) * (moe::i8_pitch(K) / moe::kI8Chunk) *
+         moe::kI8TileBytes;
+}
+
+extern "C" int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu, int8_t* q_dst,
+                               void* stream) {
+  if (!q_src || !q_dst || E < 1 || N < 1 || K < 1) return MOE_EINVAL;
+  const int64_t bytes = i8_packed_bytes(E, N, K, glu);
+  if (bytes < 0 || E > MOE_MAX_E) return MOE_ESHAPE;
+  if (((uintptr_t)q_dst) & 15) return MOE_EALIGN;
+  const int64_t lanes = bytes / 16;
+  if ((lanes + 255) / 256 > 0x7FFFFFFFLL) return MOE_ESHAPE;
+  moe::launch(moe::i8_pack_kernel, dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0,
+              (hipStream_t)stream, q_src, lanes, N, K, glu != 0, q_dst);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
+}
+
+extern "C" int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live,
+                           int64_t rows, int K, int8_t* q, float* s, void* stream) {
+  if (!x || !q || !s || rows < 1 || K < 1) return MOE_EINVAL;
+  if (x_dtype != MOE_BF16 && x_dtype != MOE_F16 && x_dtype != MOE_F32) return MOE_EINVAL;
+  if (K > MOE_I8_MAX_K || ld < K || rows > 0x7FFFFFFFLL) return MOE_ESHAPE;
+  if ((((uintptr_t)q) & 15) || (((uintptr_t)s) & 3) ||
+      (((uintptr_t)x) & (x_dtype == MOE_F32 ? 3 : 1)))
+    return MOE_EALIGN;
+  const hipStream_t st = (hipStream_t)stream;
+  if (x_dtype == MOE_BF16) return moe::launch_quantize<MOE_BF16>(x, ld, live, rows, K, q, s, st);
+  if (x_dtype == MOE_F16) return moe::launch_quantize<MOE_F16>(x, ld, live, rows, K, q, s, st);
+  return moe::launch_quantize<MOE_F32>(x, ld, live, rows, K, q, s, st);
+}
