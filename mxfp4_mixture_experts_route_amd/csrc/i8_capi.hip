@@ -2,7 +2,7 @@
 // launch. Every check runs before anything is enqueued; on failure nothing is enqueued.
 #include "i8.hpp"
 
-int moe_launch_i8_gemv(const int8_t* a, const float* as, const int32_t* a_row, int64_t a_rows,
+int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, int64_t a_rows,
                        const i8_experts* w, const int32_t* counts, const int32_t* basep,
                        int64_t rows, int64_t mpad, int act, float alpha, float limit, void* out,
                        int out_dt, int64_t ld_out, hipStream_t stream);
@@ -40,7 +40,7 @@ extern "C" int i8_gemm(const int8_t* aq, const float* as, int64_t rows, const i8
   if (w->E != 1 || ld_out < w->N || rows > 0x7FFFFFFFLL) return MOE_ESHAPE;
   st = check_align(aq, as, w, out, out_dtype);
   if (st != MOE_OK) return st;
-  return moe_launch_i8_gemv(aq, as, nullptr, rows, w, nullptr, nullptr, rows, rows, MOE_ACT_NONE,
+  return moe_launch_i8_gemm(aq, as, nullptr, rows, w, nullptr, nullptr, rows, rows, MOE_ACT_NONE,
                             0.0f, 0.0f, out, out_dtype, ld_out, (hipStream_t)stream);
 }
 
@@ -60,7 +60,7 @@ extern "C" int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_r
   const int out_dt = glu ? MOE_BF16 : MOE_F32;
   st = check_align(aq, as, w, out, out_dt);
   if (st != MOE_OK) return st;
-  return moe_launch_i8_gemv(aq, as, a_row, a_rows, w, counts, basep, 0, mpad_max, act, alpha, limit,
+  return moe_launch_i8_gemm(aq, as, a_row, a_rows, w, counts, basep, 0, mpad_max, act, alpha, limit,
                             out, out_dt, glu ? w->N / 2 : w->N, (hipStream_t)stream);
 }
 
@@ -78,7 +78,7 @@ extern "C" int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows,
   if (((uintptr_t)x) & (elem_size(x_dtype) - 1)) return MOE_EALIGN;
   st = i8_quantize(x, x_dtype, ld, nullptr, rows, w->K, q_ws, s_ws, stream);
   if (st != MOE_OK) return st;
-  return moe_launch_i8_gemv(q_ws, s_ws, nullptr, rows, w, nullptr, nullptr, rows, rows,
+  return moe_launch_i8_gemm(q_ws, s_ws, nullptr, rows, w, nullptr, nullptr, rows, rows,
                             MOE_ACT_NONE, 0.0f, 0.0f, out, out_dtype, ld_out,
                             (hipStream_t)stream);
 }
