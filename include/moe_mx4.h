@@ -521,7 +521,7 @@ int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t
  * Errors: MOE_EINVAL for NULL pointers other than d, T, E or k < 1, k > E, unknown y_dtype;
  *         MOE_ESHAPE for T > MOE_DECODE_MAX_T, k > MOE_DECODE_MAX_K, E > MOE_MAX_E, stacks that do
  *         not fit each other or E, D or F > MOE_I8_MAX_K, an expert of 2 GB or more, or
- *         T * D above about 140 000 (the quantized tokens are held in LDS); MOE_EALIGN for x, h,
+ *         T * D or T * F above about 140 000 (quantized rows are held in LDS); MOE_EALIGN for x, h,
  *         w_gu->q or w_dn->q not 16-byte aligned or other pointers not aligned to their type;
  *         MOE_ELAUNCH.
  */

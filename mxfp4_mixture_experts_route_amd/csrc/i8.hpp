@@ -63,21 +63,23 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v, int dt) 
 // value the row stands for is NaN.
 struct I8Quant {
   float s;      // the row's scale
-  float pre;    // exact power of two that lifts a tiny row (127 / m would overflow)
-  float m;      // m * pre
-  float inv;    // 127 / (m * pre), 0 for a row of zeros and for a row without a scale
+  float m;      // the largest magnitude (lifted)
+  float inv;    // 127 / m, 0 for a row of zeros and for a row without a scale
+  bool lift;    // a tiny row is lifted by 2^100, exactly: 127 / m would overflow
 
-  // mbits: largest |x| of the row as an f32 pattern (NaN and infinity are the largest of all)
+  // mbits: largest |x| of the row as an f32 pattern (NaN and infinity are the largest of all),
+  // the same on every lane of the wavefront
   __device__ __forceinline__ explicit I8Quant(uint32_t mbits) {
     const bool none = mbits >= 0x7F800000u;
     const float top = none ? 0.0f : __uint_as_float(mbits);
     s = none ? __uint_as_float(0x7FC00000u) : top / 127.0f;
-    pre = top < 0x1p-100f ? 0x1p100f : 1.0f;
-    m = top * pre;
+    lift = (uint32_t)__builtin_amdgcn_readfirstlane((int)mbits) < 0x0D800000u;   // 2^-100
+    m = lift ? top * 0x1p100f : top;
     inv = m > 0.0f ? 127.0f / m : 0.0f;
   }
 
-  // The code of x, in the low byte of the result (the rest is not cleared).
+  // The code of x (lifted), in the low byte of the result (the rest is not cleared); of no meaning
+  // in a row without a scale.
   //
   // 16-bit inputs: p = x * inv carries a relative error of at most 2^-23, that is less than 2
   // units in its last place. Where 127 x / m is a tie (j + 1/2, at most 8 significant bits) p has
@@ -85,22 +87,20 @@ struct I8Quant {
   // 2^-20 (relative) away from a tie. So p rounded to a grid of 8 units (a spacing of at most
   // 2^-20, ties of the code on the grid, the error under half of the spacing) is the tie where
   // there is one and stays on its own side elsewhere: the code is that of the exact quotient for
-  // six plain operations, where a division takes about ten.
+  // four plain operations, where a division takes about ten.
   // f32 inputs come nearer to a tie than any f32 quotient shows: there the code is checked
   // against the exact remainder in 64 bits (31 significant bits) when it is near one.
   template <int DT>
   __device__ __forceinline__ uint32_t code(float x) const {
     constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to a whole number
+    const float p = x * inv;
     if constexpr (DT != MOE_F32) {
-      const float p = (x * pre) * inv;
       const uint32_t b = (__float_as_uint(p) + 4u) & ~7u;
       return __float_as_uint(__uint_as_float(b) + kRound);
     } else {
-      const float xs = inv > 0.0f ? x * pre : 0.0f;   // a row without a scale: x may be a NaN
-      const float p = xs * inv;
       float r = rintf(p);
       if (fabsf(p - r) > 0.4999f) {
-        const double rem = 127.0 * (double)xs - (double)r * (double)m;   // exact
+        const double rem = 127.0 * (double)x - (double)r * (double)m;   // exact
         const double two = 2.0 * fabs(rem);
         const bool odd = ((int)r & 1) != 0;
         if (two > (double)m || (two == (double)m && odd)) r += rem > 0.0 ? 1.0f : -1.0f;
@@ -109,13 +109,6 @@ struct I8Quant {
     }
   }
 };
-
-// A row without a scale may hold NaN or infinity: p would be NaN and the code's bits arbitrary.
-// inv = 0 makes p 0 for every finite x; NaN and infinity are taken to 0 here.
-template <int DT>
-__device__ __forceinline__ float i8_finite(float x) {
-  return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u ? 0.0f : x;
-}
 
 // 8 values of a row at p (element index i0), zeros past n. VEC: the row is 16-byte aligned.
 template <int DT, bool VEC>
@@ -152,19 +145,23 @@ __device__ __forceinline__ uint32_t max_abs8(const float (&v)[8], uint32_t m) {
   return m;
 }
 
+// The codes of 8 values, zeros in a row without a scale (whose values may be NaN or infinite).
 template <int DT>
-__device__ __forceinline__ uint2 codes8(const I8Quant& z, const float (&v)[8]) {
+__device__ __forceinline__ uint2 codes8(const I8Quant& z, float (&v)[8]) {
   uint32_t c[8];
+  if (z.lift)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = z.code<DT>(i8_finite<DT>(v[i]));
-  uint2 o;
-  // v_perm: byte 0 of each pair, then of the pairs
+    for (int i = 0; i < 8; ++i) v[i] *= 0x1p100f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = z.code<DT>(v[i]);
+  // v_perm: the low bytes of two registers, then of two pairs
   const uint32_t a = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u);
   const uint32_t b = __builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400u);
-  o.x = __builtin_amdgcn_perm(b, a, 0x05040100u);
   const uint32_t d = __builtin_amdgcn_perm(c[5], c[4], 0x0c0c0400u);
   const uint32_t e = __builtin_amdgcn_perm(c[7], c[6], 0x0c0c0400u);
-  o.y = __builtin_amdgcn_perm(e, d, 0x05040100u);
+  uint2 o;
+  o.x = z.inv > 0.0f ? __builtin_amdgcn_perm(b, a, 0x05040100u) : 0u;
+  o.y = z.inv > 0.0f ? __builtin_amdgcn_perm(e, d, 0x05040100u) : 0u;
   return o;
 }
 
@@ -179,6 +176,91 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t m) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
   return m;
+}
+
+// LDS pitch of a quantized row: an odd multiple of 128 bytes, so that with the 16-byte pieces of
+// each 128 permuted by i8_swizzle the 16 rows of a B operand are read without bank conflicts.
+__host__ __device__ __forceinline__ int i8_lds_pitch(int KP) {
+  return (((KP + 127) >> 7) | 1) << 7;
+}
+__device__ __forceinline__ int i8_swizzle(int m, int off) { return off ^ (((m >> 1) & 7) << 4); }
+
+// A bf16 row spread over a wavefront: NV vectors of 8 values per lane, vector i of lane l holding
+// values 8 (64 i + l) .. + 7, zeros past the row. Rows of K % 8 == 0 values, 16-byte aligned.
+template <int NV>
+struct I8Row {
+  uint4 v[NV];
+  __device__ __forceinline__ void load(const uint16_t* __restrict__ row, int K) {
+    const int lane = (int)(threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int u = i * kWave + lane;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (u * 8 < K) v[i] = *reinterpret_cast<const uint4*>(row + u * 8);
+    }
+  }
+  // Largest magnitude as an f32 pattern (a bf16 pattern shifted), the same in every lane: two
+  // values a step as unsigned halves (for patterns without sign the integer order is the float's)
+  __device__ __forceinline__ uint32_t largest() const {
+    typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t m = {0, 0};
+    auto take = [&](uint32_t w) {
+      w &= 0x7FFF7FFFu;
+      u16x2_t t;
+      __builtin_memcpy(&t, &w, sizeof(t));
+      m = __builtin_elementwise_max(m, t);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      take(v[i].x);
+      take(v[i].y);
+      take(v[i].z);
+      take(v[i].w);
+    }
+    return wave_umax(max((uint32_t)m[0], (uint32_t)m[1]) << 16);
+  }
+  // Codes of the vectors i with i % parts == part (parts a power of two) into row m of an LDS
+  // image (pitch LP)
+  __device__ __forceinline__ void store_codes(const I8Quant& z, uint8_t* lds, int m, int LP, int KP,
+                                              int part, int parts) const {
+    const int lane = (int)(threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((i & (parts - 1)) != part) continue;
+      const int off = (i * kWave + lane) * 8;
+      if (off >= KP) continue;
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint2*>(lds + m * LP + i8_swizzle(m, off & ~15) + (off & 8)) =
+          codes8<MOE_BF16>(z, f);
+      __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time in registers
+    }
+  }
+};
+
+// The same for any row, read twice: its scale, and its codes into row m of an LDS image.
+__device__ __forceinline__ float i8_row_to_lds(const uint16_t* __restrict__ row, int K, uint8_t* lds,
+                                               int m, int LP, int KP) {
+  const int lane = (int)(threadIdx.x & 63);
+  uint32_t top = 0;
+  for (int u = lane; u * 8 < K; u += kWave) {
+    float t[8];
+    load8<MOE_BF16, false>(row, u * 8, K - u * 8, t);
+    top = max_abs8(t, top);
+  }
+  const I8Quant z(wave_umax(top));
+  for (int u = lane; u * 8 < KP; u += kWave) {
+    float t[8];
+    load8<MOE_BF16, false>(row, u * 8, K - u * 8, t);
+    *reinterpret_cast<uint2*>(lds + m * LP + i8_swizzle(m, (u * 8) & ~15) + ((u * 8) & 8)) =
+        codes8<MOE_BF16>(z, t);
+  }
+  return z.s;
 }
 
 }  // namespace moe

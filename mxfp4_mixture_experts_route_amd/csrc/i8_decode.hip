@@ -8,11 +8,13 @@
 //    takes the j-th picked expert with the tokens that picked it, quantizes their rows of x into
 //    LDS and runs one gate tile and its up tile over them; h is written in routed-row order, in
 //    bf16. One extra workgroup writes ids and w.
-//  * Launch 2: a workgroup owns 16 channels of every token. It finds the scale of every h row,
-//    runs the tile of each picked expert once over the rows of the tokens that picked it (h is
-//    quantized on the way into the MFMA), and sums the slots of each token in slot order.
+//  * Launch 2: a workgroup owns 16 channels of every token. It quantizes the h rows into LDS, runs
+//    the tile of each picked expert once over the rows of the tokens that picked it, and sums the
+//    slots of each token in slot order.
 // An expert is read once however many of the tokens picked it. Sums are exact integers, so the
 // results are those of i8_quantize, i8_moe_gemm and moe_combine bit for bit.
+//
+// Bound by the stream of weights: 3 D F bytes of every picked expert.
 #include "i8.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"
@@ -22,15 +24,10 @@ namespace moe {
 constexpr int kI8DecMaxR = MOE_DECODE_MAX_T * MOE_DECODE_MAX_K;   // routed rows of a call
 constexpr int kI8DecThreads = 256;
 constexpr int kI8DownThreads = 512;
-constexpr int kI8DecSeg = 8;
-constexpr size_t kI8DecMaxLds = 144 * 1024;   // the quantized tokens of launch 1
-
-// LDS pitch of a quantized row: an odd multiple of 128 bytes, so that with the pieces of 16 bytes
-// of each 128 permuted by i8_swizzle the 16 rows of a B operand are read without bank conflicts.
-__host__ __device__ __forceinline__ int i8_lds_pitch(int KP) {
-  return (((KP + 127) >> 7) | 1) << 7;
-}
-__device__ __forceinline__ int i8_swizzle(int m, int off) { return off ^ (((m >> 1) & 7) << 4); }
+constexpr int kI8UpRing = 12;       // weight chunks of a wavefront in flight, launch 1
+constexpr int kI8DownRing = 24;     // and launch 2
+constexpr int kI8DecVec = 8;        // row vectors per lane held in registers (K <= 4096)
+constexpr size_t kI8DecMaxLds = 140 * 1024;   // quantized rows in LDS
 
 // The j-th expert (ascending) of those set in a bitmap of E <= 1024 bits, or -1; every lane of
 // the calling wavefront gets it.
@@ -69,24 +66,70 @@ __device__ __forceinline__ int rows_of_expert(const int* sid, int R, int e, int*
   return n;
 }
 
-__global__ void __launch_bounds__(kI8DecThreads)
+// A run of n <= NR chunks of one weight tile: where its first chunk starts in an expert's stack.
+// A run of no chunks reads nothing (its loads are out of range and give zeros).
+struct I8Run {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off, step;
+  int n;
+};
+
+// NR chunks of a run in registers, refilled one by one from the run after it as they are used, so
+// that a wavefront has NR KB in flight from its first run to its last. Buffer loads: the
+// resource is one expert's stack and the chunk a scalar offset, so that a load takes no address
+// registers. Chunks past the end of a run are zeros, and so are their products.
+template <int NR>
+struct I8Ring {
+  u32x4_t v[NR];
+  __device__ __forceinline__ void load(int i, const I8Run& run) {
+    const uint32_t lane16 = (threadIdx.x & 63) * 16;
+    v[i] = buf_load16_nt(run.r, i < run.n ? lane16 : kOOB, i < run.n ? run.off + (uint32_t)i * run.step : 0u);
+  }
+  __device__ __forceinline__ void fill(const I8Run& run) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) load(i, run);
+  }
+  // acc += the products of the run held with the B operands from LDS row bp (its m-th row), the
+  // run's first chunk being c0; the ring is refilled from `next`
+  __device__ __forceinline__ void take(const uint8_t* bp, int m, int c0, int clast, const I8Run& next,
+                                       i32x4_t& acc, i32x4_t& acc1) {
+    const int g16 = ((int)(threadIdx.x & 63) >> 4) * 16;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const i32x4_t b = *reinterpret_cast<const i32x4_t*>(
+          bp + i8_swizzle(m, min(c0 + i, clast) * kI8Chunk + g16));
+      i32x4_t a;
+      __builtin_memcpy(&a, &v[i], sizeof(a));
+      if (i & 1)
+        acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc1, 0, 0, 0);
+      else
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
+      load(i, next);
+      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few B operands at a time
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kI8DecThreads, 4)
 i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restrict__ x, int T,
                          int E, int k, const int8_t* __restrict__ wq,
                          const float* __restrict__ wsc, const float* __restrict__ bias, int N,
-                         int K, float alpha, float limit, int units, int32_t* __restrict__ ids,
-                         float* __restrict__ w, uint16_t* __restrict__ h) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // 16 quantized rows
-  __shared__ int sid[kI8DecMaxR], list[MOE_DECODE_MAX_T];
+                         int K, float alpha, float limit, int units, int upw, int fast,
+                         int32_t* __restrict__ ids, float* __restrict__ w,
+                         uint16_t* __restrict__ h) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // quantized rows
+  constexpr int kWaves = kI8DecThreads / kWave;
+  __shared__ int sid[kI8DecMaxR], lists[kWaves][MOE_DECODE_MAX_T];
+  __shared__ uint64_t keys[kWaves][kWave];
   __shared__ float sx[MOE_DECODE_MAX_T];
   __shared__ uint32_t bits[MOE_MAX_E / 32];
-  __shared__ int sel[2];
-  __shared__ i32x4_t red[4][kWave];
-  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  __shared__ i32x4_t red[2][kWaves][kWave];
+  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int R = T * k;
 
   if (blockIdx.x == 0) {   // the routing, for the caller and for launch 2
-    for (int t = wave; t < T; t += kI8DecThreads / kWave) {
+    for (int t = wave; t < T; t += kWaves) {
       int my_id;
       float my_v;
       wave_topk(logits + (size_t)t * E, E, k, my_id, my_v);
@@ -95,88 +138,126 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     return;
   }
   const int item = (int)blockIdx.x - 1;
-  const int j = item / units, unit = item - j * units;
+  const int groups = (units + upw - 1) / upw, j = item / groups;
+  const int ubase = (item - j * groups) * upw, uend = min(ubase + upw, units);
+  const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), C = KP / kI8Chunk;
 
-  if (tid < MOE_MAX_E / 32) bits[tid] = 0u;
-  __syncthreads();
-  for (int t = wave; t < T; t += kI8DecThreads / kWave) {
-    int my_id;
-    float my_v;
-    wave_topk(logits + (size_t)t * E, E, k, my_id, my_v);
-    if (lane < k) {
-      my_id = min(max(my_id, 0), E - 1);
-      sid[t * k + lane] = my_id;
-      atomicOr(&bits[my_id >> 5], 1u << (my_id & 31));
+  // 1. routing; the only row of a single token is on its way meanwhile
+  I8Row<kI8DecVec> xr;
+  const bool early = T == 1 && fast && E <= kWave;   // (the routing of more experts needs the registers)
+  if (early) xr.load(x, K);
+  if (T > 1 && tid < MOE_MAX_E / 32) bits[tid] = 0u;
+  if (T > 1) __syncthreads();
+  if (E <= kWave) {   // a logit per lane, the rows of all of a wavefront's tokens loaded together
+    float lv[MOE_DECODE_MAX_T / kWaves];
+#pragma unroll
+    for (int i = 0; i < MOE_DECODE_MAX_T / kWaves; ++i) {
+      const int t = wave + i * kWaves;
+      lv[i] = t < T && lane < E ? logits[(size_t)t * E + lane] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < MOE_DECODE_MAX_T / kWaves; ++i) {
+      const int t = wave + i * kWaves;
+      if (t >= T) continue;
+      const int rank = wave_rank_keys(rank_key(lv[i], lane), keys[wave], E);
+      if (rank < k) {
+        sid[t * k + rank] = lane;
+        if (T > 1) atomicOr(&bits[lane >> 5], 1u << (lane & 31));
+      }
+    }
+  } else {
+    for (int t = wave; t < T; t += kWaves) {
+      int my_id;
+      float my_v;
+      wave_topk(logits + (size_t)t * E, E, k, my_id, my_v);
+      if (lane < k) {
+        my_id = min(max(my_id, 0), E - 1);
+        sid[t * k + lane] = my_id;
+        if (T > 1) atomicOr(&bits[my_id >> 5], 1u << (my_id & 31));
+      }
     }
   }
   __syncthreads();
-  if (wave == 0) {
-    const int e0 = nth_expert(bits, j);
-    const int n0 = e0 >= 0 ? rows_of_expert(sid, R, e0, list) : 0;
-    if (lane == 0) {
-      sel[0] = e0;
-      sel[1] = n0;
+  int e, cnt;
+  int* const list = lists[wave];   // a copy per wavefront: no barrier
+  if (T == 1) {                    // the picks of a token are distinct experts
+    e = sid[j];
+    cnt = 1;
+    if (lane == 0) list[0] = j;
+  } else {
+    e = nth_expert(bits, j);
+    if (e < 0) return;             // fewer experts were picked than there could have been
+    cnt = rows_of_expert(sid, R, e, list);
+  }
+  // the list is written and read by the lanes of one wavefront, whose LDS operations complete in
+  // order: only the compiler has to keep them so
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  e = __builtin_amdgcn_readfirstlane(e);
+  cnt = __builtin_amdgcn_readfirstlane(cnt);
+
+  // 2. rows of x quantized into LDS. Loads return in the order of their issue: the weights go out
+  // behind the last row, before its codes are formed
+  const int NT = i8_tiles(N, 1), HT = i8_half_tiles(N, 1);
+  const int part = wave & 1, half = (wave >> 1) ? HT : 0;
+  const int cb = C * part / 2, len = C * (part + 1) / 2 - cb;
+  const uint32_t step = (uint32_t)NT * kI8TileBytes;
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step);
+  auto run = [&](int unit, int c0) {   // the chunks of a unit's tile from c0 on
+    return I8Run{rw, ((uint32_t)(cb + c0) * NT + half + unit) * kI8TileBytes, step,
+                 unit < uend ? len - c0 : 0};
+  };
+  I8Ring<kI8UpRing> ring;
+  if (!fast) {
+    for (int m = wave; m < cnt; m += kWaves) {
+      const float s = i8_row_to_lds(x + (int64_t)(list[m] / k) * K, K, rowsq, m, LP, KP);
+      if (lane == 0) sx[m] = s;
+    }
+    ring.fill(run(ubase, 0));
+  } else {
+    // a row per wavefront; of a single row every wavefront takes a share of the codes
+    const int parts = cnt == 1 ? kWaves : 1, share = cnt == 1 ? wave : 0;
+    for (int m = cnt == 1 ? 0 : wave;; m += kWaves) {
+      if (m < cnt && !early) xr.load(x + (int64_t)(list[m] / k) * K, K);
+      if (m + kWaves >= cnt) ring.fill(run(ubase, 0));
+      if (m < cnt) {
+        const I8Quant z(xr.largest());
+        xr.store_codes(z, rowsq, m, LP, KP, share, parts);
+        if (lane == 0) sx[m] = z.s;
+      }
+      if (m + kWaves >= cnt) break;
     }
   }
   __syncthreads();
-  const int e = __builtin_amdgcn_readfirstlane(sel[0]);
-  const int cnt = __builtin_amdgcn_readfirstlane(sel[1]);
-  if (e < 0) return;   // fewer experts were picked than there could have been
 
-  const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), V = KP >> 3;
-  for (int m = wave; m < cnt; m += kI8DecThreads / kWave) {
-    const int64_t base = (int64_t)(list[m] / k) * K;
-    uint32_t top = 0;
-    for (int u = lane; u < V; u += kWave) {
-      float t[8];
-      load8<MOE_BF16, false>(x, base + u * 8, K - u * 8, t);
-      top = max_abs8(t, top);
-    }
-    const I8Quant z(wave_umax(top));
-    for (int u = lane; u < V; u += kWave) {
-      float t[8];
-      load8<MOE_BF16, false>(x, base + u * 8, K - u * 8, t);
-      const int off = u * 8;
-      *reinterpret_cast<uint2*>(rowsq + m * LP + i8_swizzle(m, off & ~15) + (off & 15)) =
-          codes8<MOE_BF16>(z, t);
-    }
-    if (lane == 0) sx[m] = z.s;
-  }
-  __syncthreads();
-
-  const int NT = i8_tiles(N, 1), HT = i8_half_tiles(N, 1), C = KP / kI8Chunk;
-  const int part = wave & 1, tile = (wave >> 1) ? HT + unit : unit;
-  const int cb = C * part / 2, ce = C * (part + 1) / 2;
-  const int64_t step = (int64_t)NT * kI8TileBytes;
-  const int8_t* wp = wq + ((int64_t)e * C * NT + tile) * kI8TileBytes + lane * 16;
+  // 3. products of the workgroup's units, one after another
+  const int F = N >> 1, jj = tid & 15, m = tid >> 4;
   const int mb = min(col, cnt - 1);   // columns past the rows repeat the last row
   const uint8_t* bp = rowsq + mb * LP;
-  i32x4_t acc = {0, 0, 0, 0};
-  for (int c0 = cb; c0 < ce; c0 += kI8DecSeg) {
-    i32x4_t wv[kI8DecSeg];
-#pragma unroll
-    for (int i = 0; i < kI8DecSeg; ++i)
-      wv[i] = *reinterpret_cast<const i32x4_t*>(wp + (int64_t)min(c0 + i, ce - 1) * step);
-#pragma unroll
-    for (int i = 0; i < kI8DecSeg; ++i)
-      if (c0 + i < ce) {
-        const i32x4_t b = *reinterpret_cast<const i32x4_t*>(
-            bp + i8_swizzle(mb, (c0 + i) * kI8Chunk + g * 16));
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], b, acc, 0, 0, 0);
-      }
-  }
-  red[wave][lane] = acc;
-  __syncthreads();
-  const int F = N >> 1, jj = tid & 15, m = tid >> 4, n = unit * 16 + jj;
-  if (m < cnt && n < F) {
-    const int from = (jj >> 2) * 16 + m, i = jj & 3;
-    const int64_t cg = (int64_t)e * N + n;
-    const float sa = sx[m];
-    const float gate = fmaf((float)(red[0][from][i] + red[1][from][i]), sa * wsc[cg],
-                            bias ? bias[cg] : 0.0f);
-    const float up = fmaf((float)(red[2][from][i] + red[3][from][i]), sa * wsc[cg + F],
-                          bias ? bias[cg + F] : 0.0f);
-    h[(int64_t)list[m] * F + n] = (uint16_t)f32_to_bf16_bits(i8_swiglu(gate, up, alpha, limit));
+  for (int unit = ubase; unit < uend; ++unit) {
+    const int n = unit * 16 + jj;
+    const int64_t cg = (int64_t)e * N + min(n, F - 1);
+    const float sg = wsc[cg], su = wsc[cg + F];
+    const float bg = bias ? bias[cg] : 0.0f, bu = bias ? bias[cg + F] : 0.0f;
+    i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+    int c0 = 0;
+    do {
+      const int cn = c0 + kI8UpRing;
+      ring.take(bp, mb, cb + c0, C - 1, cn < len ? run(unit, cn) : run(unit + 1, 0), acc, acc1);
+      c0 = cn;
+    } while (c0 < len);
+    i32x4_t (*const rd)[kWave] = red[(unit - ubase) & 1];   // two in turn: one barrier per unit
+    rd[wave][lane] = acc + acc1;
+    // a bare barrier: the ring's loads stay in flight
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (m < cnt && n < F) {
+      const int from = (jj >> 2) * 16 + m, i = jj & 3;
+      const float sa = sx[m];
+      const float gate = fmaf((float)(rd[0][from][i] + rd[1][from][i]), sa * sg, bg);
+      const float up = fmaf((float)(rd[2][from][i] + rd[3][from][i]), sa * su, bu);
+      h[(int64_t)list[m] * F + n] = (uint16_t)f32_to_bf16_bits(i8_swiglu(gate, up, alpha, limit));
+    }
   }
 }
 
@@ -184,69 +265,145 @@ __global__ void __launch_bounds__(kI8DownThreads)
 i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
                       const int32_t* __restrict__ ids, const float* __restrict__ w,
                       const int8_t* __restrict__ wq, const float* __restrict__ wsc,
-                      const float* __restrict__ bias, int D, int F, float* __restrict__ d,
-                      void* __restrict__ y, int y_dt) {
+                      const float* __restrict__ bias, int D, int F, int cap, int fast,
+                      float* __restrict__ d, void* __restrict__ y, int y_dt) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // cap quantized rows
   constexpr int kWaves = kI8DownThreads / kWave;
   __shared__ int sid[kI8DecMaxR];
+  __shared__ float sw[kI8DecMaxR];                   // routing weight of each routed row
   __shared__ float sh[kI8DecMaxR];                   // scale of each h row
-  __shared__ uint32_t top[kI8DecMaxR];               // its largest magnitude
   __shared__ int acc_s[kI8DecMaxR][kI8TileRows];     // sums of each routed row
-  __shared__ uint32_t bits[MOE_MAX_E / 32];
-  __shared__ int lists[kWaves][MOE_DECODE_MAX_T];
+  __shared__ int ord[kI8DecMaxR];                    // routed rows, those of an expert together
+  __shared__ int ex[kI8DecMaxR], start[kI8DecMaxR + 1];   // picked experts, their first places
+  __shared__ int picked_s;
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int R = T * k, unit = (int)blockIdx.x;
-  const int FP = i8_pitch(F), C = FP / kI8Chunk, NT = i8_tiles(D, 0);
-  if (tid < MOE_MAX_E / 32) bits[tid] = 0u;
+  const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = FP / kI8Chunk, NT = i8_tiles(D, 0);
+
+  // 1. the picked experts in the order of their first routed row, and the rows of each; the rows of
+  // a single token (at most one per wavefront) are on their way meanwhile
+  I8Row<kI8DecVec> hr;
+  if (T == 1 && fast && wave < R) hr.load(h + (int64_t)wave * F, F);
+  if (tid < R) {
+    sid[tid] = min(max(ids[tid], 0), E - 1);
+    sw[tid] = w[tid];
+  }
   for (int i = tid; i < R * kI8TileRows; i += kI8DownThreads) (&acc_s[0][0])[i] = 0;
   __syncthreads();
-  for (int r = tid; r < R; r += kI8DownThreads) {
-    const int e = min(max(ids[r], 0), E - 1);
-    sid[r] = e;
-    atomicOr(&bits[e >> 5], 1u << (e & 31));
-  }
-  for (int r = wave; r < R; r += kWaves) {
-    uint32_t m = 0;
-    for (int i = lane; i < F; i += kWave) m = max(m, ((uint32_t)h[(int64_t)r * F + i] << 16) & 0x7FFFFFFFu);
-    m = wave_umax(m);
-    if (lane == 0) {
-      top[r] = m;
-      sh[r] = I8Quant(m).s;
+  if (T == 1) {
+    if (tid < R) {
+      ord[tid] = tid;
+      ex[tid] = sid[tid];
     }
+    if (tid <= R) start[tid] = tid;
+    if (tid == 0) picked_s = R;
+  } else {
+    if (tid < R) {
+      const int e = sid[tid];
+      // rows of experts that come earlier, earlier rows of the same expert, earlier experts
+      int first = tid;
+      for (int r = R - 1; r >= 0; --r)
+        if (sid[r] == e) first = r;
+      ord[tid] = first;   // for now
+    }
+    __syncthreads();
+    int place = 0, rank = 0, firsts = 0;
+    if (tid < R) {
+      const int first = ord[tid];
+      for (int r = 0; r < R; ++r) {
+        const int f = ord[r];
+        place += f < first || (f == first && r < tid);
+        rank += f == r && r < first;
+        firsts += f == r;
+      }
+      if (first == tid) {
+        ex[rank] = sid[tid];
+        start[rank] = place;
+      }
+      if (tid == 0) {
+        picked_s = firsts;
+        start[firsts] = R;
+      }
+    }
+    __syncthreads();
+    if (tid < R) ord[place] = tid;
   }
   __syncthreads();
-  int picked = 0;
-  for (int i = 0; i < MOE_MAX_E / 32; ++i) picked += __popc(bits[i]);
-  constexpr int KS = 4;
-  for (int it = wave; it < picked * KS; it += kWaves) {
-    const int part = it % KS;
-    const int e = nth_expert(bits, it / KS);
-    const int cnt = rows_of_expert(sid, R, e, lists[wave]);
-    // the list is written and read by the lanes of one wavefront, whose LDS operations complete
-    // in order: only the compiler has to keep them so
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int rho = lists[wave][min(col, cnt - 1)];
-    const uint16_t* hp = h + (int64_t)rho * F;
-    const I8Quant z(top[rho]);
-    const int cb = C * part / KS, ce = C * (part + 1) / KS;
-    const int8_t* wp = wq + ((int64_t)e * C * NT + unit) * kI8TileBytes + lane * 16;
-    const int64_t step = (int64_t)NT * kI8TileBytes;
-    i32x4_t acc = {0, 0, 0, 0};
-    for (int c = cb; c < ce; ++c) {
-      const i32x4_t wv = *reinterpret_cast<const i32x4_t*>(wp + (int64_t)c * step);
-      const int k0 = c * kI8Chunk + g * 16;
-      float t0[8], t1[8];
-      load8<MOE_BF16, false>(hp, k0, F - k0, t0);
-      load8<MOE_BF16, false>(hp, k0 + 8, F - k0 - 8, t1);
-      const uint2 lo = codes8<MOE_BF16>(z, t0), hi = codes8<MOE_BF16>(z, t1);
-      const i32x4_t b = {(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, b, acc, 0, 0, 0);
+  const int picked = __builtin_amdgcn_readfirstlane(picked_s);
+
+  // 2. passes over as many experts as have their rows in LDS together; an item is one expert's
+  // tile over a segment of K
+  const int segs = (C + kI8DownRing - 1) / kI8DownRing;
+  const uint32_t step = (uint32_t)NT * kI8TileBytes;
+  auto pass_end = [&](int p0) {
+    int p1 = min(p0 + 1, picked);
+    while (p1 < picked && start[p1 + 1] - start[p0] <= cap) ++p1;
+    return __builtin_amdgcn_readfirstlane(p1);
+  };
+  // item `it` of the pass over experts [p0, p1), or the wavefront's first item of the next pass
+  auto run = [&](int p0, int p1, int it) {
+    int jx = p0 + it / segs;
+    const int seg = it % segs;
+    bool some = jx < p1;
+    if (!some && p1 < picked) {
+      jx = p1 + wave / segs;
+      some = jx < pass_end(p1);
     }
-    if (col < cnt)
+    const int sg = jx == p0 + it / segs ? seg : wave % segs;
+    const int e = some ? __builtin_amdgcn_readfirstlane(ex[jx]) : 0;
+    const int cb = C * sg / segs, ce = C * (sg + 1) / segs;
+    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step),
+                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, some ? ce - cb : 0};
+  };
+  I8Ring<kI8DownRing> ring;
+  for (int p0 = 0, p1; p0 < picked; p0 = p1) {
+    p1 = pass_end(p0);
+    const int items = (p1 - p0) * segs, row0 = start[p0], nrows = start[p1] - row0;
+    if (fast) {
+      for (int m = wave;; m += kWaves) {
+        const bool last = m + kWaves >= nrows;
+        const int rho = m < nrows ? ord[row0 + m] : -1;
+        if (rho >= 0 && T > 1) hr.load(h + (int64_t)rho * F, F);
+        if (last && p0 == 0) ring.fill(run(p0, p1, wave));
+        if (rho >= 0) {
+          const I8Quant z(hr.largest());
+          hr.store_codes(z, rowsq, m, LP, FP, 0, 1);
+          if (lane == 0) sh[rho] = z.s;
+        }
+        if (last) break;
+      }
+    } else {
+      for (int m = wave; m < nrows; m += kWaves) {
+        const int rho = ord[row0 + m];
+        const float s = i8_row_to_lds(h + (int64_t)rho * F, F, rowsq, m, LP, FP);
+        if (lane == 0) sh[rho] = s;
+      }
+      if (p0 == 0) ring.fill(run(p0, p1, wave));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // a bare barrier: the ring's loads stay
+    __builtin_amdgcn_s_barrier();                        // in flight
+    asm volatile("" ::: "memory");
+    for (int it = wave; it < items; it += kWaves) {
+      const int jx = p0 + it / segs, seg = it % segs;
+      const int cnt = start[jx + 1] - start[jx], m0 = start[jx] - row0;
+      const int mb = m0 + min(col, cnt - 1);
+      i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+      ring.take(rowsq + mb * LP, mb, C * seg / segs, C - 1, run(p0, p1, it + kWaves), acc, acc1);
+      acc += acc1;
+      if (col < cnt) {
+        const int rho = ord[start[jx] + col];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) atomicAdd(&acc_s[rho][4 * g + i], acc[i]);   // exact integers
+        for (int i = 0; i < 4; ++i) atomicAdd(&acc_s[rho][4 * g + i], acc[i]);   // exact integers
+      }
+    }
+    // the rows of this pass have been read, its sums are complete
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
-  __syncthreads();
+
+  // 3. d of every routed row, summed in slot order
   for (int i = tid; i < T * kI8TileRows; i += kI8DownThreads) {
     const int t = i >> 4, jj = i & 15, n = unit * 16 + jj;
     if (n >= D) continue;
@@ -256,7 +413,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
       const int64_t cg = (int64_t)sid[r] * D + n;
       const float dv = fmaf((float)acc_s[r][jj], sh[r] * wsc[cg], bias ? bias[cg] : 0.0f);
       if (d) d[(int64_t)r * D + n] = dv;
-      yv = fmaf(w[r], dv, yv);
+      yv = fmaf(sw[r], dv, yv);
     }
     store_elem(y, (int64_t)t * D + n, yv, y_dt);
   }
@@ -282,28 +439,43 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
       (((uintptr_t)logits) & 3) || (d && (((uintptr_t)d) & 3)) ||
       (((uintptr_t)y) & (y_dtype == MOE_F32 ? 3 : 1)))
     return MOE_EALIGN;
+  // launch 1 holds up to T quantized rows of x, launch 2 at least an expert's rows of h
   const int units = moe::i8_half_tiles(N, 1);
-  const size_t lds = (size_t)T * moe::i8_lds_pitch(moe::i8_pitch(D));
-  if (lds > moe::kI8DecMaxLds || (int64_t)units * 32 * moe::i8_pitch(D) >= (int64_t)1 << 31 ||
+  const int64_t xrow = moe::i8_lds_pitch(moe::i8_pitch(D)), hrow = moe::i8_lds_pitch(moe::i8_pitch(F));
+  if (T * xrow > (int64_t)moe::kI8DecMaxLds || T * hrow > (int64_t)moe::kI8DecMaxLds ||
+      (int64_t)units * 32 * moe::i8_pitch(D) >= (int64_t)1 << 31 ||
       (int64_t)moe::i8_tiles(D, 0) * 16 * moe::i8_pitch(F) >= (int64_t)1 << 31)
     return MOE_ESHAPE;
+  const int R = (int)T * k;
+  const size_t lds1 = (size_t)(T * xrow);
+  const int cap = (int)(R * hrow <= (int64_t)moe::kI8DecMaxLds ? R : moe::kI8DecMaxLds / hrow);
+  const size_t lds2 = (size_t)(cap * hrow);
   static bool lds_attr_set[moe::kMaxDevices] = {};   // > 64 KB of LDS: opt in once per device
   const int dslot = moe::device_slot();
-  if (lds > 65536 && (dslot < 0 || !lds_attr_set[dslot])) {
+  if (dslot < 0 || !lds_attr_set[dslot]) {
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_gate_up_kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)moe::kI8DecMaxLds) != hipSuccess ||
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_down_kernel),
                             hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)moe::kI8DecMaxLds) != hipSuccess)
       return MOE_ELAUNCH;
     if (dslot >= 0) lds_attr_set[dslot] = true;
   }
   const hipStream_t st = (hipStream_t)stream;
-  const int64_t picks = T * k < E ? T * k : E;
-  moe::launch(moe::i8_decode_gate_up_kernel, dim3((unsigned)(1 + picks * units)),
-              dim3(moe::kI8DecThreads), lds, st, logits, x, (int)T, E, k, w_gu->q, w_gu->s,
-              w_gu->bias, N, D, alpha, limit, units, ids, w, h);
+  const int fast1 = D % 8 == 0 && D <= moe::kI8DecVec * 8 * moe::kWave;
+  const int fast2 = F % 8 == 0 && F <= moe::kI8DecVec * 8 * moe::kWave;
+  const int picks = R < E ? R : E;
+  // launch 1: a resident grid (3 workgroups a CU) that takes several units each where there are
+  // more: routing and the rows' quantization are paid once per workgroup
+  const int upw = (int)(((int64_t)picks * units + 767) / 768);
+  const int groups = (units + upw - 1) / upw;
+  moe::launch(moe::i8_decode_gate_up_kernel, dim3((unsigned)(1 + picks * groups)),
+              dim3(moe::kI8DecThreads), lds1, st, logits, x, (int)T, E, k, w_gu->q, w_gu->s,
+              w_gu->bias, N, D, alpha, limit, units, upw, fast1, ids, w, h);
   if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
   moe::launch(moe::i8_decode_down_kernel, dim3((unsigned)moe::i8_tiles(D, 0)),
-              dim3(moe::kI8DownThreads), 0, st, h, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
-              w_dn->bias, D, F, d, y, y_dtype);
+              dim3(moe::kI8DownThreads), lds2, st, h, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
+              w_dn->bias, D, F, cap, fast2, d, y, y_dtype);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }
