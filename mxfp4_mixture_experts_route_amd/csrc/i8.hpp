@@ -219,6 +219,16 @@ struct I8Row {
     }
     return wave_umax(max((uint32_t)m[0], (uint32_t)m[1]) << 16);
   }
+  __device__ __forceinline__ uint2 codes(const I8Quant& z, int i) const {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+    return codes8<MOE_BF16>(z, f);
+  }
   // Codes of the vectors i with i % parts == part (parts a power of two) into row m of an LDS
   // image (pitch LP)
   __device__ __forceinline__ void store_codes(const I8Quant& z, uint8_t* lds, int m, int LP, int KP,
@@ -228,17 +238,20 @@ struct I8Row {
     for (int i = 0; i < NV; ++i) {
       if ((i & (parts - 1)) != part) continue;
       const int off = (i * kWave + lane) * 8;
-      if (off >= KP) continue;
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-      *reinterpret_cast<uint2*>(lds + m * LP + i8_swizzle(m, off & ~15) + (off & 8)) =
-          codes8<MOE_BF16>(z, f);
+      if (off < KP)
+        *reinterpret_cast<uint2*>(lds + m * LP + i8_swizzle(m, off & ~15) + (off & 8)) = codes(z, i);
       __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time in registers
+    }
+  }
+  // Codes of the vectors [u0, u1) of the row, one after another
+  __device__ __forceinline__ void store_part(const I8Quant& z, uint8_t* lds, int u0, int u1) const {
+    const int lane = (int)(threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i * kWave >= u1 || (i + 1) * kWave <= u0) continue;   // the same for the whole wavefront
+      const int u = i * kWave + lane;
+      if (u >= u0 && u < u1) *reinterpret_cast<uint2*>(lds + (u - u0) * 8) = codes(z, i);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };

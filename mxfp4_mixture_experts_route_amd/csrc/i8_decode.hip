@@ -25,9 +25,18 @@ constexpr int kI8DecMaxR = MOE_DECODE_MAX_T * MOE_DECODE_MAX_K;   // routed rows
 constexpr int kI8DecThreads = 256;
 constexpr int kI8DownThreads = 512;
 constexpr int kI8UpRing = 12;       // weight chunks of a wavefront in flight, launch 1
-constexpr int kI8DownRing = 24;     // and launch 2
+constexpr int kI8DownRing = 16;     // and launch 2
+constexpr int kI8OneRing = 12;      // launch 2 of one token
 constexpr int kI8DecVec = 8;        // row vectors per lane held in registers (K <= 4096)
 constexpr size_t kI8DecMaxLds = 140 * 1024;   // quantized rows in LDS
+
+// A barrier for what was written to LDS: loads from memory stay in flight (__syncthreads() would
+// wait for all of them).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // The j-th expert (ascending) of those set in a bitmap of E <= 1024 bits, or -1; every lane of
 // the calling wavefront gets it.
@@ -110,6 +119,168 @@ struct I8Ring {
   }
 };
 
+// ---- one token -------------------------------------------------------------------------------
+// The picks of one token are k different experts with one row each, which is the same row (launch
+// 1) or the slot's (launch 2). Every wavefront holds the whole row for its largest magnitude and
+// quantizes the part of K it multiplies into LDS of its own, so that no wavefront waits for
+// another before the sums meet; and there is little code (it is fetched anew in each launch, as
+// the two launches and what runs between them share the instruction cache).
+
+// Codes of the vectors of chunks [cb, ce) into the wavefront's LDS.
+__device__ __forceinline__ void codes_of_part(const I8Row<kI8DecVec>& row, int cb, int ce, uint8_t* lds) {
+  const I8Quant z(row.largest());
+  row.store_part(z, lds, cb * 8, ce * 8);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read by the same wavefront
+}
+
+// The expert of pick j of the token, the same on every lane.
+__device__ __forceinline__ int route_one(const float* __restrict__ logits, float lv, int E, int k,
+                                         int j, uint64_t* keys) {
+  const int lane = (int)(threadIdx.x & 63);
+  if (E <= kWave) return rank_pick(wave_rank_keys(rank_key(lv, lane), keys, E), j);
+  int my_id;
+  float my_v;
+  wave_topk(logits, E, k, my_id, my_v);
+  return min(max(__builtin_amdgcn_readlane(my_id, j), 0), E - 1);
+}
+
+// Launch 1: workgroup 0 writes the routing, the others one unit (16 gate and 16 up rows) of a pick
+// each: wavefronts {gate, up} x {halves of K}.
+__global__ void __launch_bounds__(kI8DecThreads)
+i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restrict__ x, int E, int k,
+                      const int8_t* __restrict__ wq, const float* __restrict__ wsc,
+                      const float* __restrict__ bias, int N, int K, float alpha, float limit,
+                      int units, int32_t* __restrict__ ids, float* __restrict__ w,
+                      uint16_t* __restrict__ h) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // part of the row per wavefront
+  constexpr int kWaves = kI8DecThreads / kWave;
+  __shared__ uint64_t keys[kWaves][kWave];
+  __shared__ int red[kWaves][kI8TileRows];
+  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (blockIdx.x == 0) {
+    if (wave == 0) {
+      int my_id;
+      float my_v;
+      wave_topk(logits, E, k, my_id, my_v);
+      write_topk(my_id, my_v, k, ids, w);
+    }
+    return;
+  }
+  const int item = (int)blockIdx.x - 1, j = item / units, unit = item - j * units;
+  float lv = 0.0f;
+  if (lane < E) lv = logits[lane];
+  __builtin_amdgcn_sched_barrier(0);   // the logits come first
+  I8Row<kI8DecVec> row;
+  if (E <= kWave) row.load(x, K);
+  __builtin_amdgcn_sched_barrier(0);
+  const int e = __builtin_amdgcn_readfirstlane(route_one(logits, lv, E, k, j, keys[wave]));
+  if (E > kWave) row.load(x, K);       // (the routing of more experts needs the registers)
+
+  const int C = i8_pitch(K) / kI8Chunk, NT = i8_tiles(N, 1), HT = i8_half_tiles(N, 1);
+  const int part = wave & 1, tile = (wave >> 1) ? HT + unit : unit;
+  const int cb = C * part / 2, len = C * (part + 1) / 2 - cb;
+  const uint32_t step = (uint32_t)NT * kI8TileBytes;
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step);
+  auto run = [&](int c0) {
+    return I8Run{rw, ((uint32_t)(cb + c0) * NT + tile) * kI8TileBytes, step, len - c0};
+  };
+  I8Ring<kI8UpRing> ring;
+  ring.fill(run(0));
+  const int F = N >> 1, n = unit * 16 + col;
+  const int64_t cg = (int64_t)e * N + min(n, F - 1);
+  float sg = 0.0f, su = 0.0f, bg = 0.0f, bu = 0.0f;
+  if (wave == 0) {
+    sg = wsc[cg];
+    su = wsc[cg + F];
+    if (bias) {
+      bg = bias[cg];
+      bu = bias[cg + F];
+    }
+  }
+  uint8_t* const mine = rowsq + wave * ((C + 1) / 2) * kI8Chunk;
+  codes_of_part(row, cb, cb + len, mine);
+  const I8Quant z(row.largest());
+  i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+  for (int c0 = 0; c0 < len; c0 += kI8UpRing)
+    ring.take(mine, 0, c0, max(len - 1, 0), run(c0 + kI8UpRing), acc, acc1);
+  acc += acc1;
+  if (col == 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][4 * g + i] = acc[i];
+  lds_barrier();
+  if (tid < kI8TileRows && n < F) {
+    const float gate = fmaf((float)(red[0][tid] + red[1][tid]), z.s * sg, bg);
+    const float up = fmaf((float)(red[2][tid] + red[3][tid]), z.s * su, bu);
+    h[(int64_t)j * F + n] = (uint16_t)f32_to_bf16_bits(i8_swiglu(gate, up, alpha, limit));
+  }
+}
+
+// Launch 2: a workgroup owns 16 channels; wavefronts {slots} x {parts of K}.
+__global__ void __launch_bounds__(1024)
+i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
+                   const int32_t* __restrict__ ids, const float* __restrict__ w,
+                   const int8_t* __restrict__ wq, const float* __restrict__ wsc,
+                   const float* __restrict__ bias, int D, int F, float* __restrict__ d,
+                   void* __restrict__ y, int y_dt) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // part of a row per wavefront
+  __shared__ int red[16][kI8TileRows];
+  __shared__ float dv_s[MOE_DECODE_MAX_K][kI8TileRows];
+  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int unit = (int)blockIdx.x, slot = wave / parts, part = wave - slot * parts;
+  int e = ids[slot];
+  const float wt = w[slot];
+  __builtin_amdgcn_sched_barrier(0);   // the id comes first
+  I8Row<kI8DecVec> row;
+  row.load(h + (int64_t)slot * F, F);
+  __builtin_amdgcn_sched_barrier(0);
+  e = __builtin_amdgcn_readfirstlane(min(max(e, 0), E - 1));
+  const int C = i8_pitch(F) / kI8Chunk, NT = i8_tiles(D, 0);
+  const int cb = C * part / parts, len = C * (part + 1) / parts - cb;
+  const uint32_t step = (uint32_t)NT * kI8TileBytes;
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step);
+  auto run = [&](int c0) {
+    return I8Run{rw, ((uint32_t)(cb + c0) * NT + unit) * kI8TileBytes, step, len - c0};
+  };
+  I8Ring<kI8OneRing> ring;
+  ring.fill(run(0));
+  const int n = unit * 16 + col;
+  const int64_t cg = (int64_t)e * D + min(n, D - 1);
+  float sc = 0.0f, bi = 0.0f;
+  if (part == 0) {
+    sc = wsc[cg];
+    if (bias) bi = bias[cg];
+  }
+  uint8_t* const mine = rowsq + wave * ((C + parts - 1) / parts) * kI8Chunk;
+  codes_of_part(row, cb, cb + len, mine);
+  const I8Quant z(row.largest());
+  i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+  for (int c0 = 0; c0 < len; c0 += kI8OneRing)
+    ring.take(mine, 0, c0, max(len - 1, 0), run(c0 + kI8OneRing), acc, acc1);
+  acc += acc1;
+  if (col == 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][4 * g + i] = acc[i];
+  lds_barrier();
+  if (part == 0 && lane < kI8TileRows) {
+    int sum = 0;
+    for (int p = 0; p < parts; ++p) sum += red[wave + p][lane];
+    const float dv = fmaf((float)sum, z.s * sc, bi);
+    if (d && n < D) d[(int64_t)slot * D + n] = dv;
+    dv_s[slot][lane] = wt;
+    red[wave][lane] = __float_as_int(dv);
+  }
+  lds_barrier();
+  if (tid < kI8TileRows && n < D) {
+    float yv = 0.0f;
+    for (int s = 0; s < k; ++s) yv = fmaf(dv_s[s][tid], __int_as_float(red[s * parts][tid]), yv);
+    store_elem(y, n, yv, y_dt);
+  }
+}
+
+// ---- several tokens --------------------------------------------------------------------------
+
 __global__ void __launch_bounds__(kI8DecThreads, 4)
 i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restrict__ x, int T,
                          int E, int k, const int8_t* __restrict__ wq,
@@ -142,18 +313,16 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   const int ubase = (item - j * groups) * upw, uend = min(ubase + upw, units);
   const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), C = KP / kI8Chunk;
 
-  // 1. routing; the only row of a single token is on its way meanwhile
-  I8Row<kI8DecVec> xr;
-  const bool early = T == 1 && fast && E <= kWave;   // (the routing of more experts needs the registers)
-  if (early) xr.load(x, K);
-  if (T > 1 && tid < MOE_MAX_E / 32) bits[tid] = 0u;
-  if (T > 1) __syncthreads();
+  // 1. routing
+  if (tid < MOE_MAX_E / 32) bits[tid] = 0u;
+  lds_barrier();
   if (E <= kWave) {   // a logit per lane, the rows of all of a wavefront's tokens loaded together
     float lv[MOE_DECODE_MAX_T / kWaves];
 #pragma unroll
     for (int i = 0; i < MOE_DECODE_MAX_T / kWaves; ++i) {
       const int t = wave + i * kWaves;
-      lv[i] = t < T && lane < E ? logits[(size_t)t * E + lane] : 0.0f;
+      lv[i] = 0.0f;
+      if (t < T && lane < E) lv[i] = logits[(size_t)t * E + lane];
     }
 #pragma unroll
     for (int i = 0; i < MOE_DECODE_MAX_T / kWaves; ++i) {
@@ -162,7 +331,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
       const int rank = wave_rank_keys(rank_key(lv[i], lane), keys[wave], E);
       if (rank < k) {
         sid[t * k + rank] = lane;
-        if (T > 1) atomicOr(&bits[lane >> 5], 1u << (lane & 31));
+        atomicOr(&bits[lane >> 5], 1u << (lane & 31));
       }
     }
   } else {
@@ -173,22 +342,15 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
       if (lane < k) {
         my_id = min(max(my_id, 0), E - 1);
         sid[t * k + lane] = my_id;
-        if (T > 1) atomicOr(&bits[my_id >> 5], 1u << (my_id & 31));
+        atomicOr(&bits[my_id >> 5], 1u << (my_id & 31));
       }
     }
   }
-  __syncthreads();
-  int e, cnt;
+  lds_barrier();
   int* const list = lists[wave];   // a copy per wavefront: no barrier
-  if (T == 1) {                    // the picks of a token are distinct experts
-    e = sid[j];
-    cnt = 1;
-    if (lane == 0) list[0] = j;
-  } else {
-    e = nth_expert(bits, j);
-    if (e < 0) return;             // fewer experts were picked than there could have been
-    cnt = rows_of_expert(sid, R, e, list);
-  }
+  int e = nth_expert(bits, j);
+  if (e < 0) return;               // fewer experts were picked than there could have been
+  int cnt = rows_of_expert(sid, R, e, list);
   // the list is written and read by the lanes of one wavefront, whose LDS operations complete in
   // order: only the compiler has to keep them so
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -207,6 +369,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
                  unit < uend ? len - c0 : 0};
   };
   I8Ring<kI8UpRing> ring;
+  I8Row<kI8DecVec> xr;
   if (!fast) {
     for (int m = wave; m < cnt; m += kWaves) {
       const float s = i8_row_to_lds(x + (int64_t)(list[m] / k) * K, K, rowsq, m, LP, KP);
@@ -217,7 +380,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     // a row per wavefront; of a single row every wavefront takes a share of the codes
     const int parts = cnt == 1 ? kWaves : 1, share = cnt == 1 ? wave : 0;
     for (int m = cnt == 1 ? 0 : wave;; m += kWaves) {
-      if (m < cnt && !early) xr.load(x + (int64_t)(list[m] / k) * K, K);
+      if (m < cnt) xr.load(x + (int64_t)(list[m] / k) * K, K);
       if (m + kWaves >= cnt) ring.fill(run(ubase, 0));
       if (m < cnt) {
         const I8Quant z(xr.largest());
@@ -227,7 +390,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
       if (m + kWaves >= cnt) break;
     }
   }
-  __syncthreads();
+  lds_barrier();
 
   // 3. products of the workgroup's units, one after another
   const int F = N >> 1, jj = tid & 15, m = tid >> 4;
@@ -247,10 +410,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     } while (c0 < len);
     i32x4_t (*const rd)[kWave] = red[(unit - ubase) & 1];   // two in turn: one barrier per unit
     rd[wave][lane] = acc + acc1;
-    // a bare barrier: the ring's loads stay in flight
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    lds_barrier();
     if (m < cnt && n < F) {
       const int from = (jj >> 2) * 16 + m, i = jj & 3;
       const float sa = sx[m];
@@ -272,7 +432,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
   __shared__ int sid[kI8DecMaxR];
   __shared__ float sw[kI8DecMaxR];                   // routing weight of each routed row
   __shared__ float sh[kI8DecMaxR];                   // scale of each h row
-  __shared__ int acc_s[kI8DecMaxR][kI8TileRows];     // sums of each routed row
+  __shared__ int acc_s[kI8DecMaxR][kI8TileRows];     // sums of each routed row, then its d (f32)
   __shared__ int ord[kI8DecMaxR];                    // routed rows, those of an expert together
   __shared__ int ex[kI8DecMaxR], start[kI8DecMaxR + 1];   // picked experts, their first places
   __shared__ int picked_s;
@@ -281,91 +441,95 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
   const int R = T * k, unit = (int)blockIdx.x;
   const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = FP / kI8Chunk, NT = i8_tiles(D, 0);
 
-  // 1. the picked experts in the order of their first routed row, and the rows of each; the rows of
-  // a single token (at most one per wavefront) are on their way meanwhile
-  I8Row<kI8DecVec> hr;
-  if (T == 1 && fast && wave < R) hr.load(h + (int64_t)wave * F, F);
+  // 1. the picked experts in the order of their first routed row, and the rows of each
+  const int segs = (C + kI8DownRing - 1) / kI8DownRing;
+  const uint32_t step = (uint32_t)NT * kI8TileBytes;
+  auto run = [&](int e, int seg, bool some) {   // expert e's tile over a segment of K
+    const int cb = C * seg / segs, ce = C * (seg + 1) / segs;
+    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step),
+                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, some ? ce - cb : 0};
+  };
+  I8Ring<kI8DownRing> ring;
   if (tid < R) {
     sid[tid] = min(max(ids[tid], 0), E - 1);
     sw[tid] = w[tid];
   }
   for (int i = tid; i < R * kI8TileRows; i += kI8DownThreads) (&acc_s[0][0])[i] = 0;
-  __syncthreads();
-  if (T == 1) {
-    if (tid < R) {
-      ord[tid] = tid;
-      ex[tid] = sid[tid];
-    }
-    if (tid <= R) start[tid] = tid;
-    if (tid == 0) picked_s = R;
-  } else {
-    if (tid < R) {
-      const int e = sid[tid];
-      // rows of experts that come earlier, earlier rows of the same expert, earlier experts
-      int first = tid;
-      for (int r = R - 1; r >= 0; --r)
-        if (sid[r] == e) first = r;
-      ord[tid] = first;   // for now
-    }
-    __syncthreads();
-    int place = 0, rank = 0, firsts = 0;
-    if (tid < R) {
-      const int first = ord[tid];
-      for (int r = 0; r < R; ++r) {
-        const int f = ord[r];
-        place += f < first || (f == first && r < tid);
-        rank += f == r && r < first;
-        firsts += f == r;
-      }
-      if (first == tid) {
-        ex[rank] = sid[tid];
-        start[rank] = place;
-      }
-      if (tid == 0) {
-        picked_s = firsts;
-        start[firsts] = R;
-      }
-    }
-    __syncthreads();
-    if (tid < R) ord[place] = tid;
+  lds_barrier();
+  if (tid < R) {
+    const int e = sid[tid];
+    // rows of experts that come earlier, earlier rows of the same expert, earlier experts
+    int first = tid;
+    for (int r = R - 1; r >= 0; --r)
+      if (sid[r] == e) first = r;
+    ord[tid] = first;   // for now
   }
-  __syncthreads();
+  lds_barrier();
+  int place = 0, rank = 0, firsts = 0;
+  if (tid < R) {
+    const int first = ord[tid];
+    for (int r = 0; r < R; ++r) {
+      const int f = ord[r];
+      place += f < first || (f == first && r < tid);
+      rank += f == r && r < first;
+      firsts += f == r;
+    }
+    if (first == tid) {
+      ex[rank] = sid[tid];
+      start[rank] = place;
+    }
+    if (tid == 0) {
+      picked_s = firsts;
+      start[firsts] = R;
+    }
+  }
+  lds_barrier();
+  if (tid < R) ord[place] = tid;
+  lds_barrier();
   const int picked = __builtin_amdgcn_readfirstlane(picked_s);
+
+  // scales and biases of the sums this thread turns into d: channel tid % 16 of rows tid / 16 + 32 i
+  const int jj = tid & 15, n = unit * 16 + jj;
+  float dsc[kI8DecMaxR * kI8TileRows / kI8DownThreads], dbi[kI8DecMaxR * kI8TileRows / kI8DownThreads];
+#pragma unroll
+  for (int i = 0; i < kI8DecMaxR * kI8TileRows / kI8DownThreads; ++i) {
+    const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
+    dsc[i] = dbi[i] = 0.0f;
+    if (r < R && n < D) {
+      const int64_t cg = (int64_t)sid[r] * D + n;
+      dsc[i] = wsc[cg];
+      if (bias) dbi[i] = bias[cg];
+    }
+  }
 
   // 2. passes over as many experts as have their rows in LDS together; an item is one expert's
   // tile over a segment of K
-  const int segs = (C + kI8DownRing - 1) / kI8DownRing;
-  const uint32_t step = (uint32_t)NT * kI8TileBytes;
   auto pass_end = [&](int p0) {
     int p1 = min(p0 + 1, picked);
     while (p1 < picked && start[p1 + 1] - start[p0] <= cap) ++p1;
     return __builtin_amdgcn_readfirstlane(p1);
   };
   // item `it` of the pass over experts [p0, p1), or the wavefront's first item of the next pass
-  auto run = [&](int p0, int p1, int it) {
-    int jx = p0 + it / segs;
-    const int seg = it % segs;
+  auto item = [&](int p0, int p1, int it) {
+    int jx = p0 + it / segs, seg = it % segs;
     bool some = jx < p1;
     if (!some && p1 < picked) {
       jx = p1 + wave / segs;
+      seg = wave % segs;
       some = jx < pass_end(p1);
     }
-    const int sg = jx == p0 + it / segs ? seg : wave % segs;
-    const int e = some ? __builtin_amdgcn_readfirstlane(ex[jx]) : 0;
-    const int cb = C * sg / segs, ce = C * (sg + 1) / segs;
-    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step),
-                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, some ? ce - cb : 0};
+    return run(some ? __builtin_amdgcn_readfirstlane(ex[jx]) : 0, seg, some);
   };
-  I8Ring<kI8DownRing> ring;
   for (int p0 = 0, p1; p0 < picked; p0 = p1) {
     p1 = pass_end(p0);
     const int items = (p1 - p0) * segs, row0 = start[p0], nrows = start[p1] - row0;
     if (fast) {
+      I8Row<kI8DecVec> hr;
       for (int m = wave;; m += kWaves) {
         const bool last = m + kWaves >= nrows;
         const int rho = m < nrows ? ord[row0 + m] : -1;
-        if (rho >= 0 && T > 1) hr.load(h + (int64_t)rho * F, F);
-        if (last && p0 == 0) ring.fill(run(p0, p1, wave));
+        if (rho >= 0) hr.load(h + (int64_t)rho * F, F);
+        if (last && p0 == 0) ring.fill(item(p0, p1, wave));
         if (rho >= 0) {
           const I8Quant z(hr.largest());
           hr.store_codes(z, rowsq, m, LP, FP, 0, 1);
@@ -379,17 +543,15 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
         const float s = i8_row_to_lds(h + (int64_t)rho * F, F, rowsq, m, LP, FP);
         if (lane == 0) sh[rho] = s;
       }
-      if (p0 == 0) ring.fill(run(p0, p1, wave));
+      if (p0 == 0) ring.fill(item(p0, p1, wave));
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // a bare barrier: the ring's loads stay
-    __builtin_amdgcn_s_barrier();                        // in flight
-    asm volatile("" ::: "memory");
+    lds_barrier();
     for (int it = wave; it < items; it += kWaves) {
       const int jx = p0 + it / segs, seg = it % segs;
       const int cnt = start[jx + 1] - start[jx], m0 = start[jx] - row0;
       const int mb = m0 + min(col, cnt - 1);
       i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
-      ring.take(rowsq + mb * LP, mb, C * seg / segs, C - 1, run(p0, p1, it + kWaves), acc, acc1);
+      ring.take(rowsq + mb * LP, mb, C * seg / segs, C - 1, item(p0, p1, it + kWaves), acc, acc1);
       acc += acc1;
       if (col < cnt) {
         const int rho = ord[start[jx] + col];
@@ -397,24 +559,23 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
         for (int i = 0; i < 4; ++i) atomicAdd(&acc_s[rho][4 * g + i], acc[i]);   // exact integers
       }
     }
-    // the rows of this pass have been read, its sums are complete
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    lds_barrier();   // the rows of this pass have been read, its sums are complete
   }
 
   // 3. d of every routed row, summed in slot order
-  for (int i = tid; i < T * kI8TileRows; i += kI8DownThreads) {
-    const int t = i >> 4, jj = i & 15, n = unit * 16 + jj;
-    if (n >= D) continue;
+#pragma unroll
+  for (int i = 0; i < kI8DecMaxR * kI8TileRows / kI8DownThreads; ++i) {
+    const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
+    if (r >= R) break;
+    const float dv = fmaf((float)acc_s[r][jj], sh[r] * dsc[i], dbi[i]);
+    if (d && n < D) d[(int64_t)r * D + n] = dv;
+    acc_s[r][jj] = __float_as_int(dv);
+  }
+  lds_barrier();
+  if (tid < T * kI8TileRows && n < D) {
+    const int t = tid >> 4;
     float yv = 0.0f;
-    for (int s = 0; s < k; ++s) {
-      const int r = t * k + s;
-      const int64_t cg = (int64_t)sid[r] * D + n;
-      const float dv = fmaf((float)acc_s[r][jj], sh[r] * wsc[cg], bias ? bias[cg] : 0.0f);
-      if (d) d[(int64_t)r * D + n] = dv;
-      yv = fmaf(sw[r], dv, yv);
-    }
+    for (int s = 0; s < k; ++s) yv = fmaf(sw[t * k + s], __int_as_float(acc_s[t * k + s][jj]), yv);
     store_elem(y, (int64_t)t * D + n, yv, y_dt);
   }
 }
@@ -465,6 +626,21 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
   const hipStream_t st = (hipStream_t)stream;
   const int fast1 = D % 8 == 0 && D <= moe::kI8DecVec * 8 * moe::kWave;
   const int fast2 = F % 8 == 0 && F <= moe::kI8DecVec * 8 * moe::kWave;
+  if (T == 1 && fast1 && fast2) {
+    const int Cd = moe::i8_pitch(D) / moe::kI8Chunk, Cf = moe::i8_pitch(F) / moe::kI8Chunk;
+    // launch 2: 16 wavefronts, or as many as there are slots and chunks for
+    int parts = 16 / k;
+    while (parts > 1 && Cf < 4 * parts) --parts;
+    moe::launch(moe::i8_one_gate_up_kernel, dim3((unsigned)(1 + k * units)), dim3(moe::kI8DecThreads),
+                (size_t)(4 * ((Cd + 1) / 2) * moe::kI8Chunk), st, logits, x, E, k, w_gu->q, w_gu->s,
+                w_gu->bias, N, D, alpha, limit, units, ids, w, h);
+    if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
+    moe::launch(moe::i8_one_down_kernel, dim3((unsigned)moe::i8_tiles(D, 0)),
+                dim3((unsigned)(64 * k * parts)),
+                (size_t)(k * parts * ((Cf + parts - 1) / parts) * moe::kI8Chunk), st, h, E, k, parts,
+                ids, w, w_dn->q, w_dn->s, w_dn->bias, D, F, d, y, y_dtype);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
+  }
   const int picks = R < E ? R : E;
   // launch 1: a resident grid (3 workgroups a CU) that takes several units each where there are
   // more: routing and the rows' quantization are paid once per workgroup
