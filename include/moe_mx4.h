@@ -511,24 +511,29 @@ int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t
                 int64_t mpad_max, int act, float alpha, float limit, void* out, void* stream);
 
 /*
- * The whole layer of a few tokens in two launches ([chain] in this format): what
+ * The whole layer of a few tokens in two launches, or three for T*k > 16 ([chain] in this format;
+ * the third quantizes h, which launch 2 otherwise does on the way): what
  * moe_route_topk, i8_quantize, i8_moe_gemm with MOE_ACT_SWIGLU_OAI, i8_quantize,
  * i8_moe_gemm with MOE_ACT_NONE and moe_combine compute, bit for bit, with h and d by routed row
  * rho = t*k + s. An expert is read once however many of the tokens picked it.
  *   logits f32 [T][E];  x bf16 [T][D];  w_gu: glu = 1, N = 2F, K = D;  w_dn: glu = 0, N = D, K = F
  *   ids i32 [T][k], w f32 [T][k] out (as moe_route_topk);  h bf16 [T*k][F] out
+ *   q_ws int8 [T*k][roundup(F, 64)], s_ws f32 [T*k]: scratch that the call may write and leaves
+ *   without meaning; both may be NULL for T*k <= 16 and F <= 4096. Calls that can run concurrently
+ *   need distinct scratch.
  *   d f32 [T*k][D] out or NULL (then never written);  y y_dtype [T][D] out
- * Errors: MOE_EINVAL for NULL pointers other than d, T, E or k < 1, k > E, unknown y_dtype;
+ * Errors: MOE_EINVAL for NULL pointers other than d (q_ws and s_ws: where they are needed), T, E or
+ *         k < 1, k > E, unknown y_dtype;
  *         MOE_ESHAPE for T > MOE_DECODE_MAX_T, k > MOE_DECODE_MAX_K, E > MOE_MAX_E, stacks that do
  *         not fit each other or E, D or F > MOE_I8_MAX_K, an expert of 2 GB or more, or
- *         T * D or T * F above about 140 000 (quantized rows are held in LDS); MOE_EALIGN for x, h,
- *         w_gu->q or w_dn->q not 16-byte aligned or other pointers not aligned to their type;
+ *         T * D above about 140 000 (the quantized tokens are held in LDS); MOE_EALIGN for x, h,
+ *         q_ws, w_gu->q or w_dn->q not 16-byte aligned or other pointers not aligned to their type;
  *         MOE_ELAUNCH.
  */
 int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, int E, int k,
                   const i8_experts* w_gu, const i8_experts* w_dn, float alpha, float limit,
-                  int32_t* ids, float* w, uint16_t* h, float* d, void* y, int y_dtype,
-                  void* stream);
+                  int32_t* ids, float* w, uint16_t* h, int8_t* q_ws, float* s_ws, float* d, void* y,
+                  int y_dtype, void* stream);
 
 /*
  * Router-weighted combine ([chain]: routing-weighted sum of the expert rows in slot order).

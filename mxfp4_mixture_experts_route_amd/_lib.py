@@ -123,8 +123,8 @@ def lib() -> ctypes.CDLL:
         L.i8_moe_gemm.restype = ci
         L.i8_moe_gemm.argtypes = [vp, vp, vp, i64, p8, vp, vp, ci, i64, ci, cf, cf, vp, vp]
         L.i8_moe_decode.restype = ci
-        L.i8_moe_decode.argtypes = [vp, vp, i64, ci, ci, p8, p8, cf, cf, vp, vp, vp, vp, vp, ci,
-                                    vp]
+        L.i8_moe_decode.argtypes = [vp, vp, i64, ci, ci, p8, p8, cf, cf, vp, vp, vp, vp, vp, vp, vp,
+                                    ci, vp]
         _lib = L
     return _lib
 
@@ -679,10 +679,13 @@ def i8_moe_gemm(aq, as_, a_row, w: I8Experts, counts, basep, tile_m: int, mpad_m
 
 
 def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha: float = 1.702,
-                  limit: float = 7.0, want_d: bool = False, y_dtype=None, out=None, stream=None):
-    """The whole 8-bit layer of a few tokens (two launches). Returns a dict with ids, w [T][k], h
-    bf16 [T*k][F] and d f32 [T*k][D] in routed-row order (d only with want_d), and y [T][D] in
-    y_dtype (f32 by default). `out` may hold preallocated tensors under those keys."""
+                  limit: float = 7.0, want_d: bool = False, y_dtype=None, out=None, ws=None,
+                  stream=None):
+    """The whole 8-bit layer of a few tokens (two launches; three for T*k > 16). Returns a dict with
+    ids, w [T][k], h bf16 [T*k][F] and d f32 [T*k][D] in routed-row order (d only with want_d), and
+    y [T][D] in y_dtype (f32 by default). `out` may hold preallocated tensors under those keys. ws:
+    scratch of i8_row_buffers(T*k, F) (allocated if needed); concurrent calls need distinct
+    scratch."""
     torch = _torch()
     _check(logits, torch.float32, "logits")
     _check(x, torch.bfloat16, "x")
@@ -703,10 +706,17 @@ def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha:
             _i8_out(o[key], shape, dt, key)
         else:
             o[key] = torch.empty(shape, dtype=dt, device=x.device)
-    _same_device(x, logits, gate_up, down, *(o[key] for key in shapes))
+    if ws is not None:
+        _i8_out(ws[0], (T * k, i8_pitch(F)), torch.int8, "ws[0]")
+        _i8_out(ws[1], (T * k,), torch.float32, "ws[1]")
+    elif T * k > 16 or F > 4096:
+        ws = i8_row_buffers(T * k, F, x.device)
+    else:
+        ws = (None, None)
+    _same_device(x, logits, gate_up, down, ws[0], ws[1], *(o[key] for key in shapes))
     _i8_call("i8_moe_decode", x.device, stream, _ptr(logits), _ptr(x), T, E, k, gate_up.ref,
              down.ref, float(alpha), float(limit), _ptr(o["ids"]), _ptr(o["w"]), _ptr(o["h"]),
-             _ptr(o.get("d")), _ptr(o["y"]), _i8_dtype(y_dtype, "y"))
+             _ptr(ws[0]), _ptr(ws[1]), _ptr(o.get("d")), _ptr(o["y"]), _i8_dtype(y_dtype, "y"))
     return o
 
 

@@ -26,7 +26,9 @@ constexpr int kI8DecThreads = 256;
 constexpr int kI8DownThreads = 512;
 constexpr int kI8UpRing = 12;       // weight chunks of a wavefront in flight, launch 1
 constexpr int kI8DownRing = 16;     // and launch 2
+constexpr int kI8RowsRing = 12;     // launch 2 over quantized rows (as many of the rows')
 constexpr int kI8OneRing = 12;      // launch 2 of one token
+constexpr int kI8LdsRows = 16;      // h rows that launch 2 quantizes itself
 constexpr int kI8DecVec = 8;        // row vectors per lane held in registers (K <= 4096)
 constexpr size_t kI8DecMaxLds = 140 * 1024;   // quantized rows in LDS
 
@@ -75,7 +77,7 @@ __device__ __forceinline__ int rows_of_expert(const int* sid, int R, int e, int*
   return n;
 }
 
-// A run of n <= NR chunks of one weight tile: where its first chunk starts in an expert's stack.
+// A run of n <= NR chunks of 16 weight rows: where its first chunk starts in an expert's stack.
 // A run of no chunks reads nothing (its loads are out of range and give zeros).
 struct I8Run {
   __amdgpu_buffer_rsrc_t r;
@@ -90,9 +92,10 @@ struct I8Run {
 template <int NR>
 struct I8Ring {
   u32x4_t v[NR];
+  uint32_t voff;   // the lane's place in a chunk: its number times 16 where the rows are a tile
+  __device__ __forceinline__ explicit I8Ring(uint32_t lane_off) : voff(lane_off) {}
   __device__ __forceinline__ void load(int i, const I8Run& run) {
-    const uint32_t lane16 = (threadIdx.x & 63) * 16;
-    v[i] = buf_load16_nt(run.r, i < run.n ? lane16 : kOOB, i < run.n ? run.off + (uint32_t)i * run.step : 0u);
+    v[i] = buf_load16_nt(run.r, i < run.n ? voff : kOOB, i < run.n ? run.off + (uint32_t)i * run.step : 0u);
   }
   __device__ __forceinline__ void fill(const I8Run& run) {
 #pragma unroll
@@ -185,7 +188,7 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   auto run = [&](int c0) {
     return I8Run{rw, ((uint32_t)(cb + c0) * NT + tile) * kI8TileBytes, step, len - c0};
   };
-  I8Ring<kI8UpRing> ring;
+  I8Ring<kI8UpRing> ring(lane * 16);
   ring.fill(run(0));
   const int F = N >> 1, n = unit * 16 + col;
   const int64_t cg = (int64_t)e * N + min(n, F - 1);
@@ -216,9 +219,41 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   }
 }
 
-// Launch 2: a workgroup owns 16 channels; wavefronts {slots} x {parts of K}.
+// Channels of a workgroup of launch 2. One CU takes in about 26 KB/us of weights (11 B a clock),
+// so the launch lasts as long as the CU with the most channels: with 16 each, 2880 channels keep
+// 180 of the 256 CUs busy, with 12 each 240 (16 tokens: 55.6 -> SPAN16 us). Fewer than 16 channels
+// leave rows of the MFMA operand empty, which costs nothing here.
+inline int down_span(int D) {
+  int best = 16, most = 0x7FFFFFFF;
+  for (int span = 16; span >= 4; span -= 4) {
+    const int units = (D + span - 1) / span, crit = (units + 255) / 256 * span;
+    if (crit < most) {
+      most = crit;
+      best = span;
+    }
+  }
+  return best;
+}
+
+// The lane's place in a chunk of the weights: row lane % 16 of the span's, from channel n0 on,
+// may lie in two tiles; lanes past the span or the last channel read nothing.
+__device__ __forceinline__ uint32_t span_lane(int n0, int span, int D) {
+  const int lane = (int)(threadIdx.x & 63), r = lane & 15, n = n0 + r;
+  return r < span && n < D
+             ? (uint32_t)((n >> 4) * kI8TileBytes + (lane >> 4) * 256 + (n & 15) * 16)
+             : kOOB;
+}
+
+// Neighbouring units share cache lines where a span is not a whole tile: they go to one XCD
+// (workgroups are dealt to the 8 XCDs round robin).
+__device__ __forceinline__ int xcd_unit(int units) {
+  const int per = (units + 7) >> 3, x = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3;
+  return i < per && x * per + i < units ? x * per + i : -1;
+}
+
+// Launch 2: a workgroup owns `span` channels; wavefronts {slots} x {parts of K}.
 __global__ void __launch_bounds__(1024)
-i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
+i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts, int span, int units,
                    const int32_t* __restrict__ ids, const float* __restrict__ w,
                    const int8_t* __restrict__ wq, const float* __restrict__ wsc,
                    const float* __restrict__ bias, int D, int F, float* __restrict__ d,
@@ -228,7 +263,8 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
   __shared__ float dv_s[MOE_DECODE_MAX_K][kI8TileRows];
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int unit = (int)blockIdx.x, slot = wave / parts, part = wave - slot * parts;
+  const int unit = xcd_unit(units), slot = wave / parts, part = wave - slot * parts;
+  if (unit < 0) return;
   int e = ids[slot];
   const float wt = w[slot];
   __builtin_amdgcn_sched_barrier(0);   // the id comes first
@@ -241,11 +277,11 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step);
   auto run = [&](int c0) {
-    return I8Run{rw, ((uint32_t)(cb + c0) * NT + unit) * kI8TileBytes, step, len - c0};
+    return I8Run{rw, (uint32_t)(cb + c0) * step, step, len - c0};
   };
-  I8Ring<kI8OneRing> ring;
+  I8Ring<kI8OneRing> ring(span_lane(unit * span, span, D));
   ring.fill(run(0));
-  const int n = unit * 16 + col;
+  const int n = unit * span + col;
   const int64_t cg = (int64_t)e * D + min(n, D - 1);
   float sc = 0.0f, bi = 0.0f;
   if (part == 0) {
@@ -263,7 +299,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][4 * g + i] = acc[i];
   lds_barrier();
-  if (part == 0 && lane < kI8TileRows) {
+  if (part == 0 && lane < span) {
     int sum = 0;
     for (int p = 0; p < parts; ++p) sum += red[wave + p][lane];
     const float dv = fmaf((float)sum, z.s * sc, bi);
@@ -272,7 +308,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
     red[wave][lane] = __float_as_int(dv);
   }
   lds_barrier();
-  if (tid < kI8TileRows && n < D) {
+  if (tid < span && n < D) {
     float yv = 0.0f;
     for (int s = 0; s < k; ++s) yv = fmaf(dv_s[s][tid], __int_as_float(red[s * parts][tid]), yv);
     store_elem(y, n, yv, y_dt);
@@ -368,7 +404,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     return I8Run{rw, ((uint32_t)(cb + c0) * NT + half + unit) * kI8TileBytes, step,
                  unit < uend ? len - c0 : 0};
   };
-  I8Ring<kI8UpRing> ring;
+  I8Ring<kI8UpRing> ring(lane * 16);
   I8Row<kI8DecVec> xr;
   if (!fast) {
     for (int m = wave; m < cnt; m += kWaves) {
@@ -421,150 +457,180 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   }
 }
 
+// The picked experts of launch 2 in the order of their first routed row, and the rows of each.
+struct I8Picks {
+  int sid[kI8DecMaxR];                         // expert of each routed row
+  float sw[kI8DecMaxR];                        // its routing weight
+  int ord[kI8DecMaxR];                         // routed rows, those of an expert together
+  int ex[kI8DecMaxR], start[kI8DecMaxR + 1];   // picked experts, their first places in ord
+  int picked;
+
+  __device__ __forceinline__ void build(const int32_t* __restrict__ ids, const float* __restrict__ w,
+                                        int R, int E) {
+    const int tid = (int)threadIdx.x;
+    if (tid < R) {
+      sid[tid] = min(max(ids[tid], 0), E - 1);
+      sw[tid] = w[tid];
+    }
+    lds_barrier();
+    if (tid < R) {   // the first row of the same expert, for now in ord
+      int first = tid;
+      for (int r = R - 1; r >= 0; --r)
+        if (sid[r] == sid[tid]) first = r;
+      ord[tid] = first;
+    }
+    lds_barrier();
+    int place = 0, rank = 0, firsts = 0;
+    if (tid < R) {
+      const int first = ord[tid];
+      for (int r = 0; r < R; ++r) {
+        const int f = ord[r];
+        place += f < first || (f == first && r < tid);
+        rank += f == r && r < first;
+        firsts += f == r;
+      }
+      if (first == tid) {
+        ex[rank] = sid[tid];
+        start[rank] = place;
+      }
+      if (tid == 0) {
+        picked = firsts;
+        start[firsts] = R;
+      }
+    }
+    lds_barrier();
+    if (tid < R) ord[place] = tid;
+    lds_barrier();
+  }
+};
+
+// Launch 2 of several tokens. ROWS: the h rows come quantized (hq, hs) and go to the MFMA straight
+// from memory; otherwise (few rows) every workgroup quantizes all of them into LDS first.
+template <bool ROWS>
 __global__ void __launch_bounds__(kI8DownThreads)
-i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
+i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__ hq,
+                      const float* __restrict__ hs, int T, int E, int k,
                       const int32_t* __restrict__ ids, const float* __restrict__ w,
                       const int8_t* __restrict__ wq, const float* __restrict__ wsc,
-                      const float* __restrict__ bias, int D, int F, int cap, int fast,
+                      const float* __restrict__ bias, int D, int F, int fast, int span, int units,
                       float* __restrict__ d, void* __restrict__ y, int y_dt) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // cap quantized rows
+  extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // R quantized rows, or none
   constexpr int kWaves = kI8DownThreads / kWave;
-  __shared__ int sid[kI8DecMaxR];
-  __shared__ float sw[kI8DecMaxR];                   // routing weight of each routed row
+  constexpr int NR = ROWS ? kI8RowsRing : kI8DownRing;
+  constexpr int kSums = kI8DecMaxR * kI8TileRows / kI8DownThreads;   // sums of a thread
+  __shared__ I8Picks p;
   __shared__ float sh[kI8DecMaxR];                   // scale of each h row
   __shared__ int acc_s[kI8DecMaxR][kI8TileRows];     // sums of each routed row, then its d (f32)
-  __shared__ int ord[kI8DecMaxR];                    // routed rows, those of an expert together
-  __shared__ int ex[kI8DecMaxR], start[kI8DecMaxR + 1];   // picked experts, their first places
-  __shared__ int picked_s;
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int R = T * k, unit = (int)blockIdx.x;
+  const int R = T * k, unit = xcd_unit(units);
+  if (unit < 0) return;
   const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = FP / kI8Chunk, NT = i8_tiles(D, 0);
 
-  // 1. the picked experts in the order of their first routed row, and the rows of each
-  const int segs = (C + kI8DownRing - 1) / kI8DownRing;
-  const uint32_t step = (uint32_t)NT * kI8TileBytes;
-  auto run = [&](int e, int seg, bool some) {   // expert e's tile over a segment of K
-    const int cb = C * seg / segs, ce = C * (seg + 1) / segs;
-    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step),
-                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, some ? ce - cb : 0};
-  };
-  I8Ring<kI8DownRing> ring;
-  if (tid < R) {
-    sid[tid] = min(max(ids[tid], 0), E - 1);
-    sw[tid] = w[tid];
-  }
   for (int i = tid; i < R * kI8TileRows; i += kI8DownThreads) (&acc_s[0][0])[i] = 0;
-  lds_barrier();
-  if (tid < R) {
-    const int e = sid[tid];
-    // rows of experts that come earlier, earlier rows of the same expert, earlier experts
-    int first = tid;
-    for (int r = R - 1; r >= 0; --r)
-      if (sid[r] == e) first = r;
-    ord[tid] = first;   // for now
+  if (ROWS && tid < R) sh[tid] = hs[tid];
+  p.build(ids, w, R, E);
+  const int picked = __builtin_amdgcn_readfirstlane(p.picked);
+
+  // an item is one picked expert's rows of the span over a segment of K
+  const int segs = (C + NR - 1) / NR, items = picked * segs;
+  const uint32_t step = (uint32_t)NT * kI8TileBytes;
+  auto run = [&](int it) {
+    const int jx = it / segs, seg = it - jx * segs;
+    const int cb = C * seg / segs, ce = C * (seg + 1) / segs;
+    const int e = it < items ? __builtin_amdgcn_readfirstlane(p.ex[jx]) : 0;
+    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step), (uint32_t)cb * step, step,
+                 it < items ? ce - cb : 0};
+  };
+  // ROWS: the lane's row and piece of the item's activations, behind which its segment's chunks lie
+  auto rows = [&](int it) {
+    const int jx = min(it, items - 1) / segs;
+    const int m = p.start[jx] + min(col, p.start[jx + 1] - p.start[jx] - 1);
+    return (uint32_t)(p.ord[m] * FP + g * 16);
+  };
+  I8Ring<NR> ring(span_lane(unit * span, span, D));
+  u32x4_t bv[ROWS ? NR : 1];
+  const __amdgpu_buffer_rsrc_t rh = make_rsrc(hq, ROWS ? (uint32_t)(R * FP) : 0u);
+  if constexpr (ROWS) {
+    ring.fill(run(wave));
+    const uint32_t bo = rows(wave);
+    const int c0 = C * (wave % segs) / segs;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) bv[i] = buf_load16(rh, bo, (uint32_t)min(c0 + i, C - 1) * kI8Chunk);
+  } else {
+    if (fast) {   // loads return in the order of their issue: the weights go behind the last row
+      I8Row<kI8DecVec> hr;
+      for (int m = wave;; m += kWaves) {
+        const bool last = m + kWaves >= R;
+        if (m < R) hr.load(h + (int64_t)p.ord[m] * F, F);
+        if (last) ring.fill(run(wave));
+        if (m < R) {
+          const I8Quant z(hr.largest());
+          hr.store_codes(z, rowsq, m, LP, FP, 0, 1);
+          if (lane == 0) sh[p.ord[m]] = z.s;
+        }
+        if (last) break;
+      }
+    } else {
+      for (int m = wave; m < R; m += kWaves) {
+        const float s = i8_row_to_lds(h + (int64_t)p.ord[m] * F, F, rowsq, m, LP, FP);
+        if (lane == 0) sh[p.ord[m]] = s;
+      }
+      ring.fill(run(wave));
+    }
+    lds_barrier();
   }
-  lds_barrier();
-  int place = 0, rank = 0, firsts = 0;
-  if (tid < R) {
-    const int first = ord[tid];
-    for (int r = 0; r < R; ++r) {
-      const int f = ord[r];
-      place += f < first || (f == first && r < tid);
-      rank += f == r && r < first;
-      firsts += f == r;
-    }
-    if (first == tid) {
-      ex[rank] = sid[tid];
-      start[rank] = place;
-    }
-    if (tid == 0) {
-      picked_s = firsts;
-      start[firsts] = R;
-    }
-  }
-  lds_barrier();
-  if (tid < R) ord[place] = tid;
-  lds_barrier();
-  const int picked = __builtin_amdgcn_readfirstlane(picked_s);
 
   // scales and biases of the sums this thread turns into d: channel tid % 16 of rows tid / 16 + 32 i
-  const int jj = tid & 15, n = unit * 16 + jj;
-  float dsc[kI8DecMaxR * kI8TileRows / kI8DownThreads], dbi[kI8DecMaxR * kI8TileRows / kI8DownThreads];
+  const int jj = tid & 15, n = jj < span ? unit * span + jj : D;   // D: none
+  float dsc[kSums], dbi[kSums];
 #pragma unroll
-  for (int i = 0; i < kI8DecMaxR * kI8TileRows / kI8DownThreads; ++i) {
+  for (int i = 0; i < kSums; ++i) {
     const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
     dsc[i] = dbi[i] = 0.0f;
     if (r < R && n < D) {
-      const int64_t cg = (int64_t)sid[r] * D + n;
+      const int64_t cg = (int64_t)p.sid[r] * D + n;
       dsc[i] = wsc[cg];
       if (bias) dbi[i] = bias[cg];
     }
   }
 
-  // 2. passes over as many experts as have their rows in LDS together; an item is one expert's
-  // tile over a segment of K
-  auto pass_end = [&](int p0) {
-    int p1 = min(p0 + 1, picked);
-    while (p1 < picked && start[p1 + 1] - start[p0] <= cap) ++p1;
-    return __builtin_amdgcn_readfirstlane(p1);
-  };
-  // item `it` of the pass over experts [p0, p1), or the wavefront's first item of the next pass
-  auto item = [&](int p0, int p1, int it) {
-    int jx = p0 + it / segs, seg = it % segs;
-    bool some = jx < p1;
-    if (!some && p1 < picked) {
-      jx = p1 + wave / segs;
-      seg = wave % segs;
-      some = jx < pass_end(p1);
-    }
-    return run(some ? __builtin_amdgcn_readfirstlane(ex[jx]) : 0, seg, some);
-  };
-  for (int p0 = 0, p1; p0 < picked; p0 = p1) {
-    p1 = pass_end(p0);
-    const int items = (p1 - p0) * segs, row0 = start[p0], nrows = start[p1] - row0;
-    if (fast) {
-      I8Row<kI8DecVec> hr;
-      for (int m = wave;; m += kWaves) {
-        const bool last = m + kWaves >= nrows;
-        const int rho = m < nrows ? ord[row0 + m] : -1;
-        if (rho >= 0) hr.load(h + (int64_t)rho * F, F);
-        if (last && p0 == 0) ring.fill(item(p0, p1, wave));
-        if (rho >= 0) {
-          const I8Quant z(hr.largest());
-          hr.store_codes(z, rowsq, m, LP, FP, 0, 1);
-          if (lane == 0) sh[rho] = z.s;
-        }
-        if (last) break;
+  for (int it = wave; it < items; it += kWaves) {
+    const int jx = it / segs, seg = it - jx * segs;
+    const int cnt = p.start[jx + 1] - p.start[jx], m0 = p.start[jx];
+    const I8Run next = run(it + kWaves);
+    i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+    if constexpr (ROWS) {
+      const uint32_t bo = rows(it + kWaves);
+      const int cn = C * ((it + kWaves) % segs) / segs;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        i32x4_t a, b;
+        __builtin_memcpy(&a, &ring.v[i], sizeof(a));
+        __builtin_memcpy(&b, &bv[i], sizeof(b));
+        if (i & 1)
+          acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc1, 0, 0, 0);
+        else
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
+        ring.load(i, next);
+        bv[i] = buf_load16(rh, bo, (uint32_t)min(cn + i, C - 1) * kI8Chunk);
       }
     } else {
-      for (int m = wave; m < nrows; m += kWaves) {
-        const int rho = ord[row0 + m];
-        const float s = i8_row_to_lds(h + (int64_t)rho * F, F, rowsq, m, LP, FP);
-        if (lane == 0) sh[rho] = s;
-      }
-      if (p0 == 0) ring.fill(item(p0, p1, wave));
-    }
-    lds_barrier();
-    for (int it = wave; it < items; it += kWaves) {
-      const int jx = p0 + it / segs, seg = it % segs;
-      const int cnt = start[jx + 1] - start[jx], m0 = start[jx] - row0;
       const int mb = m0 + min(col, cnt - 1);
-      i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
-      ring.take(rowsq + mb * LP, mb, C * seg / segs, C - 1, item(p0, p1, it + kWaves), acc, acc1);
-      acc += acc1;
-      if (col < cnt) {
-        const int rho = ord[start[jx] + col];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) atomicAdd(&acc_s[rho][4 * g + i], acc[i]);   // exact integers
-      }
+      ring.take(rowsq + mb * LP, mb, C * seg / segs, C - 1, next, acc, acc1);
     }
-    lds_barrier();   // the rows of this pass have been read, its sums are complete
-  }
-
-  // 3. d of every routed row, summed in slot order
+    acc += acc1;
+    if (col < cnt) {
+      const int rho = p.ord[m0 + col];
 #pragma unroll
-  for (int i = 0; i < kI8DecMaxR * kI8TileRows / kI8DownThreads; ++i) {
+      for (int i = 0; i < 4; ++i) atomicAdd(&acc_s[rho][4 * g + i], acc[i]);   // exact integers
+    }
+  }
+  lds_barrier();
+
+  // d of every routed row, summed in slot order
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) {
     const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
     if (r >= R) break;
     const float dv = fmaf((float)acc_s[r][jj], sh[r] * dsc[i], dbi[i]);
@@ -575,7 +641,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
   if (tid < T * kI8TileRows && n < D) {
     const int t = tid >> 4;
     float yv = 0.0f;
-    for (int s = 0; s < k; ++s) yv = fmaf(sw[t * k + s], __int_as_float(acc_s[t * k + s][jj]), yv);
+    for (int s = 0; s < k; ++s) yv = fmaf(p.sw[t * k + s], __int_as_float(acc_s[t * k + s][jj]), yv);
     store_elem(y, (int64_t)t * D + n, yv, y_dt);
   }
 }
@@ -584,8 +650,8 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, int T, int E, int k,
 
 extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, int E, int k,
                              const i8_experts* w_gu, const i8_experts* w_dn, float alpha,
-                             float limit, int32_t* ids, float* w, uint16_t* h, float* d, void* y,
-                             int y_dtype, void* stream) {
+                             float limit, int32_t* ids, float* w, uint16_t* h, int8_t* q_ws, float* s_ws,
+                             float* d, void* y, int y_dtype, void* stream) {
   if (!logits || !x || !w_gu || !w_dn || !ids || !w || !h || !y || !w_gu->q || !w_gu->s ||
       !w_dn->q || !w_dn->s || T < 1 || E < 1 || k < 1 || k > E)
     return MOE_EINVAL;
@@ -600,24 +666,26 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
       (((uintptr_t)logits) & 3) || (d && (((uintptr_t)d) & 3)) ||
       (((uintptr_t)y) & (y_dtype == MOE_F32 ? 3 : 1)))
     return MOE_EALIGN;
-  // launch 1 holds up to T quantized rows of x, launch 2 at least an expert's rows of h
-  const int units = moe::i8_half_tiles(N, 1);
+  // launch 1 holds up to T quantized rows of x in LDS, launch 2 those of h where they are few
+  const int R = (int)T * k, units = moe::i8_half_tiles(N, 1);
   const int64_t xrow = moe::i8_lds_pitch(moe::i8_pitch(D)), hrow = moe::i8_lds_pitch(moe::i8_pitch(F));
-  if (T * xrow > (int64_t)moe::kI8DecMaxLds || T * hrow > (int64_t)moe::kI8DecMaxLds ||
+  if (T * xrow > (int64_t)moe::kI8DecMaxLds ||
       (int64_t)units * 32 * moe::i8_pitch(D) >= (int64_t)1 << 31 ||
       (int64_t)moe::i8_tiles(D, 0) * 16 * moe::i8_pitch(F) >= (int64_t)1 << 31)
     return MOE_ESHAPE;
-  const int R = (int)T * k;
-  const size_t lds1 = (size_t)(T * xrow);
-  const int cap = (int)(R * hrow <= (int64_t)moe::kI8DecMaxLds ? R : moe::kI8DecMaxLds / hrow);
-  const size_t lds2 = (size_t)(cap * hrow);
+  const bool own_rows = R <= moe::kI8LdsRows && R * hrow <= (int64_t)moe::kI8DecMaxLds;
+  if (!own_rows) {
+    if (!q_ws || !s_ws) return MOE_EINVAL;
+    if ((((uintptr_t)q_ws) & 15) || (((uintptr_t)s_ws) & 3)) return MOE_EALIGN;
+  }
+  const size_t lds1 = (size_t)(T * xrow), lds2 = own_rows ? (size_t)(R * hrow) : 0;
   static bool lds_attr_set[moe::kMaxDevices] = {};   // > 64 KB of LDS: opt in once per device
   const int dslot = moe::device_slot();
   if (dslot < 0 || !lds_attr_set[dslot]) {
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_gate_up_kernel),
                             hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)moe::kI8DecMaxLds) != hipSuccess ||
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_down_kernel),
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_down_kernel<false>),
                             hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)moe::kI8DecMaxLds) != hipSuccess)
       return MOE_ELAUNCH;
@@ -626,6 +694,7 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
   const hipStream_t st = (hipStream_t)stream;
   const int fast1 = D % 8 == 0 && D <= moe::kI8DecVec * 8 * moe::kWave;
   const int fast2 = F % 8 == 0 && F <= moe::kI8DecVec * 8 * moe::kWave;
+  const int span = moe::down_span(D), dunits = (D + span - 1) / span;
   if (T == 1 && fast1 && fast2) {
     const int Cd = moe::i8_pitch(D) / moe::kI8Chunk, Cf = moe::i8_pitch(F) / moe::kI8Chunk;
     // launch 2: 16 wavefronts, or as many as there are slots and chunks for
@@ -635,23 +704,43 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
                 (size_t)(4 * ((Cd + 1) / 2) * moe::kI8Chunk), st, logits, x, E, k, w_gu->q, w_gu->s,
                 w_gu->bias, N, D, alpha, limit, units, ids, w, h);
     if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
-    moe::launch(moe::i8_one_down_kernel, dim3((unsigned)moe::i8_tiles(D, 0)),
+    moe::launch(moe::i8_one_down_kernel, dim3((unsigned)((dunits + 7) / 8 * 8)),
                 dim3((unsigned)(64 * k * parts)),
                 (size_t)(k * parts * ((Cf + parts - 1) / parts) * moe::kI8Chunk), st, h, E, k, parts,
-                ids, w, w_dn->q, w_dn->s, w_dn->bias, D, F, d, y, y_dtype);
+                span, dunits, ids, w, w_dn->q, w_dn->s, w_dn->bias, D, F, d, y, y_dtype);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
   }
   const int picks = R < E ? R : E;
-  // launch 1: a resident grid (3 workgroups a CU) that takes several units each where there are
-  // more: routing and the rows' quantization are paid once per workgroup
-  const int upw = (int)(((int64_t)picks * units + 767) / 768);
+  // launch 1: units per workgroup. Routing and the rows' quantization are paid once per workgroup,
+  // so it takes as many units as it needs for the expected number of picked experts to fill the
+  // resident workgroups once (3 a CU, fewer where LDS holds fewer), and an odd number: with 4 or 8
+  // the workgroups start on strides of a power of two and meet on the same memory channels (16
+  // tokens, 32 experts: 5 units 70 us, 4 83 us, 8 93 us, 1 106 us; 8 tokens: 51, 60, 57, 55 us)
+  double none = 1.0;   // an expert's chance to be picked by no token
+  for (int t = 0; t < T; ++t) none *= 1.0 - (double)k / E;
+  const double live = E * (1.0 - none);
+  const int fit = (int)((160 * 1024) / (lds1 + 12 * 1024));
+  const double slots = 256.0 * (fit < 3 ? fit : 3);
+  int upw = 1;
+  while (upw < units && live * ((units + upw - 1) / upw) > slots) upw += 2;
   const int groups = (units + upw - 1) / upw;
   moe::launch(moe::i8_decode_gate_up_kernel, dim3((unsigned)(1 + picks * groups)),
               dim3(moe::kI8DecThreads), lds1, st, logits, x, (int)T, E, k, w_gu->q, w_gu->s,
               w_gu->bias, N, D, alpha, limit, units, upw, fast1, ids, w, h);
   if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
-  moe::launch(moe::i8_decode_down_kernel, dim3((unsigned)moe::i8_tiles(D, 0)),
-              dim3(moe::kI8DownThreads), lds2, st, h, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
-              w_dn->bias, D, F, cap, fast2, d, y, y_dtype);
+  const dim3 grid2((unsigned)((dunits + 7) / 8 * 8));
+  if (own_rows) {
+    moe::launch(moe::i8_decode_down_kernel<false>, grid2, dim3(moe::kI8DownThreads), lds2, st, h,
+                (const int8_t*)nullptr, (const float*)nullptr, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
+                w_dn->bias, D, F, fast2, span, dunits, d, y, y_dtype);
+  } else {
+    // every workgroup of launch 2 would quantize every row, some 2 us for 8 of them: more than 16
+    // rows are quantized once, by a launch of its own
+    const int qs = i8_quantize(h, MOE_BF16, F, nullptr, R, F, q_ws, s_ws, stream);
+    if (qs != MOE_OK) return qs;
+    moe::launch(moe::i8_decode_down_kernel<true>, grid2, dim3(moe::kI8DownThreads), 0, st, h,
+                (const int8_t*)q_ws, (const float*)s_ws, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
+                w_dn->bias, D, F, fast2, span, dunits, d, y, y_dtype);
+  }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }

@@ -167,9 +167,9 @@ def test_decode_argument_checks():
     f = _lib.lib().i8_moe_decode
     gu, dn = stack(E=4, N=96, K=100, glu=1), stack(E=4, N=100, K=48)
 
-    def call(logits=FAKE, x=FAKE, T=2, E=4, k=2, gu=gu, dn=dn, ids=FAKE, w=FAKE, h=FAKE, d=None,
-             y=FAKE, dt=F32):
-        return f(logits, x, T, E, k, ref(gu), ref(dn), 1.702, 7.0, ids, w, h, d, y, dt, None)
+    def call(logits=FAKE, x=FAKE, T=2, E=4, k=2, gu=gu, dn=dn, ids=FAKE, w=FAKE, h=FAKE, q=FAKE,
+             s=FAKE, d=None, y=FAKE, dt=F32):
+        return f(logits, x, T, E, k, ref(gu), ref(dn), 1.702, 7.0, ids, w, h, q, s, d, y, dt, None)
 
     for name in ("logits", "x", "gu", "dn", "ids", "w", "h", "y"):
         assert call(**{name: None}) == EINVAL, name
@@ -185,6 +185,10 @@ def test_decode_argument_checks():
     assert call(dn=stack(E=4, N=99, K=48)) == ESHAPE
     assert call(dn=stack(E=4, N=100, K=47)) == ESHAPE
     assert call(T=16, gu=stack(E=4, N=96, K=10000, glu=1), dn=stack(E=4, N=10000, K=48)) == ESHAPE
+    assert call(T=9, q=None) == EINVAL                             # 18 rows of h need scratch
+    assert call(T=9, s=None) == EINVAL
+    assert call(T=9, q=OFF[8]) == EALIGN
+    assert call(T=9, s=OFF[2]) == EALIGN
     assert call(x=OFF[8]) == EALIGN
     assert call(h=OFF[8]) == EALIGN
     assert call(logits=OFF[2]) == EALIGN
