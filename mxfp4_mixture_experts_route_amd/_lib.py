@@ -8,6 +8,7 @@ library is missing, loading fails with an error that says how to build it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -472,48 +473,75 @@ def mx4_moe_decode_persistent_static(logits, x, gate_up: MX4Experts, down: MX4Ex
 # 8-bit integer projections
 # ---------------------------------------------------------------------------------------------
 
+_i8_codes = {}   # torch dtype -> moe_dtype
+_i8_fns = {}     # C entry points by name
+
+
 def _i8_dtype(dtype, name: str) -> int:
-    torch = _torch()
-    code = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}.get(dtype)
+    if not _i8_codes:
+        torch = _torch()
+        _i8_codes.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16,
+                          torch.float32: MOE_F32})
+    code = _i8_codes.get(dtype)
     if code is None:
         raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
     return code
 
 
-def _same_device(first, *others) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-
-
-def _i8_call(fn: str, device, stream, *args):
-    """The C entry point on `stream` (by default the device's current one), with that device
-    current: a tensor of another device than the current one runs on its own."""
+def _i8_call(fn: str, dev: int, stream, *args) -> None:
+    """The C entry point on `stream` (by default the current one of device `dev`), with that
+    device current: tensors of another device than the current one are worked on there."""
     torch = _torch()
-    with torch.cuda.device(device):
-        _call(fn, *args, _stream(stream))
+    f = _i8_fns.get(fn)
+    if f is None:
+        f = _i8_fns[fn] = getattr(lib(), fn)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    if st != MOE_OK:
+        raise MoeError(fn, st)
 
 
-def _i8_rows(x, name: str, dtype=None) -> int:
-    """Checks a matrix of rows whose elements are contiguous; returns its row pitch (elements)."""
-    if dtype is not None and x.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
-    if x.device.type != "cuda":
+def _i8_rows(x, name: str) -> int:
+    """Checks a device matrix of rows whose elements are contiguous; returns its row pitch in
+    elements."""
+    if not x.is_cuda:
         raise TypeError(f"{name}: expected a device tensor")
     if x.dim() != 2:
         raise ValueError(f"{name}: expected a matrix of rows, got shape {tuple(x.shape)}")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    rows, n = x.shape
+    ld, one = x.stride()
+    if n > 1 and one != 1:
         raise ValueError(f"{name}: expected rows of contiguous elements")
-    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {x.stride(0)} of {x.shape[1]} elements)")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    if rows < 2:
+        return n
+    if ld < n:
+        raise ValueError(f"{name}: rows overlap (stride {ld} of {n} elements)")
+    return ld
 
 
-def _i8_out(out, shape, dtype, name: str):
-    """Checks an output of the caller's: contiguous, of this shape and type."""
-    _check(out, dtype, name)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+def _i8_check(t, shape, dtype, name: str, dev: int) -> None:
+    """Checks a contiguous tensor of this shape and type on device number `dev`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a device tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the others on {dev}")
+
+
+def _i8_weights(w, name: str, dev: int) -> None:
+    if not isinstance(w, I8Experts):
+        raise TypeError(f"{name}: expected I8Experts, got {type(w).__name__}")
+    if w.dev != dev:
+        raise ValueError(f"{name}: on device {w.dev}, the others on {dev}")
 
 
 def i8_pitch(K: int) -> int:
@@ -539,30 +567,27 @@ class I8Experts:
     def __init__(self, q, s, bias=None, glu: bool = False, stream=None):
         torch = _torch()
         _check(q, torch.int8, "q")
-        _check(s, torch.float32, "s")
         if q.dim() == 2:
             q = q.unsqueeze(0)
         if q.dim() != 3:
             raise ValueError(f"q: expected shape [E][N][K] or [N][K], got {tuple(q.shape)}")
         E, N, K = q.shape
-        s = s.reshape(1, -1) if s.dim() == 1 else s
-        if tuple(s.shape) != (E, N):
-            raise ValueError(f"s: expected shape {(E, N)}, got {tuple(s.shape)}")
+        dev = q.get_device()
+        if s.dim() == 1:
+            s = s.unsqueeze(0)
+        _i8_check(s, (E, N), torch.float32, "s", dev)
         if bias is not None:
-            _check(bias, torch.float32, "bias")
-            bias = bias.reshape(1, -1) if bias.dim() == 1 else bias
-            if tuple(bias.shape) != (E, N):
-                raise ValueError(f"bias: expected shape {(E, N)}, got {tuple(bias.shape)}")
-        _same_device(q, s, bias)
+            if bias.dim() == 1:
+                bias = bias.unsqueeze(0)
+            _i8_check(bias, (E, N), torch.float32, "bias", dev)
         glu = int(bool(glu))
         nbytes = int(lib().i8_packed_bytes(E, N, K, glu))
         if nbytes < 0:
             raise MoeError("i8_pack_experts", MOE_ESHAPE)
         qp = torch.empty(nbytes, dtype=torch.int8, device=q.device)
-        _i8_call("i8_pack_experts", q.device, stream, _ptr(q), E, N, K, glu, _ptr(qp))
-        self.q, self.s, self.bias = qp, s, bias
+        _i8_call("i8_pack_experts", dev, stream, q.data_ptr(), E, N, K, glu, qp.data_ptr())
+        self.q, self.s, self.bias, self.dev = qp, s, bias, dev
         self.E, self.N, self.K, self.glu = E, N, K, glu
-        self.device = q.device
         self.c = I8ExpertsC(qp.data_ptr(), s.data_ptr(),
                             None if bias is None else bias.data_ptr(), E, N, K, glu)
         self.ref = ctypes.byref(self.c)
@@ -588,29 +613,31 @@ def i8_quantize(x, live=None, out=None, stream=None):
     ld = _i8_rows(x, "x")
     code = _i8_dtype(x.dtype, "x")
     rows, K = x.shape
+    dev = x.get_device()
     if live is not None:
-        _i8_out(live, (rows,), torch.int32, "live")
+        _i8_check(live, (rows,), torch.int32, "live", dev)
     if out is None:
         out = i8_row_buffers(rows, K, x.device)
     else:
-        _i8_out(out[0], (rows, i8_pitch(K)), torch.int8, "q")
-        _i8_out(out[1], (rows,), torch.float32, "s")
+        _i8_check(out[0], (rows, i8_pitch(K)), torch.int8, "q", dev)
+        _i8_check(out[1], (rows,), torch.float32, "s", dev)
     q, s = out
-    _same_device(x, live, q, s)
-    _i8_call("i8_quantize", x.device, stream, _ptr(x), code, ld, _ptr(live), rows, K, _ptr(q),
-             _ptr(s))
+    _i8_call("i8_quantize", dev, stream, x.data_ptr(), code, ld,
+             None if live is None else live.data_ptr(), rows, K, q.data_ptr(), s.data_ptr())
     return q, s
 
 
-def _i8_dense_out(out, rows: int, w, out_dtype, device):
-    torch = _torch()
+def _i8_dense_out(out, rows: int, w, out_dtype, x, dev: int):
     if out is None:
-        out = torch.empty((rows, w.N), dtype=out_dtype or torch.bfloat16, device=device)
-    elif out_dtype is not None and out.dtype != out_dtype:
+        out = _torch().empty((rows, w.N), dtype=out_dtype, device=x.device)
+        return out, _i8_dtype(out_dtype, "out"), w.N
+    if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
     ld = _i8_rows(out, "out")
-    if tuple(out.shape) != (rows, w.N):
+    if out.shape != (rows, w.N):
         raise ValueError(f"out: expected shape {(rows, w.N)}, got {tuple(out.shape)}")
+    if out.get_device() != dev:
+        raise ValueError(f"out: on device {out.get_device()}, the others on {dev}")
     return out, _i8_dtype(out.dtype, "out"), ld
 
 
@@ -618,12 +645,15 @@ def i8_gemm(aq, as_, w: I8Experts, out_dtype=None, out=None, stream=None):
     """Dense product of quantized rows (aq, as_) with the one matrix of w: out [rows][N] in
     out_dtype (bf16 by default) or in `out` (any row stride)."""
     torch = _torch()
-    rows = aq.shape[0]
-    _i8_out(aq, (rows, i8_pitch(w.K)), torch.int8, "aq")
-    _i8_out(as_, (rows,), torch.float32, "as")
-    out, code, ld = _i8_dense_out(out, rows, w, out_dtype, aq.device)
-    _same_device(aq, as_, out, w)
-    _i8_call("i8_gemm", aq.device, stream, _ptr(aq), _ptr(as_), rows, w.ref, _ptr(out), code, ld)
+    rows, dev = aq.shape[0], aq.get_device()
+    _i8_weights(w, "w", dev)
+    _i8_check(aq, (rows, i8_pitch(w.K)), torch.int8, "aq", dev)
+    _i8_check(as_, (rows,), torch.float32, "as", dev)
+    if out is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    out, code, ld = _i8_dense_out(out, rows, w, out_dtype, aq, dev)
+    _i8_call("i8_gemm", dev, stream, aq.data_ptr(), as_.data_ptr(), rows, w.ref, out.data_ptr(),
+             code, ld)
     return out
 
 
@@ -635,19 +665,20 @@ def i8_linear(x, w: I8Experts, out_dtype=None, out=None, ws=None, stream=None):
     ld = _i8_rows(x, "x")
     code = _i8_dtype(x.dtype, "x")
     rows, K = x.shape
+    dev = x.get_device()
+    _i8_weights(w, "w", dev)
     if K != w.K:
         raise ValueError(f"x: expected rows of {w.K} values, got {K}")
     if ws is None:
         ws = i8_row_buffers(rows, K, x.device)
     else:
-        _i8_out(ws[0], (rows, i8_pitch(K)), torch.int8, "ws[0]")
-        _i8_out(ws[1], (rows,), torch.float32, "ws[1]")
+        _i8_check(ws[0], (rows, i8_pitch(K)), torch.int8, "ws[0]", dev)
+        _i8_check(ws[1], (rows,), torch.float32, "ws[1]", dev)
     if out is None and out_dtype is None:
         out_dtype = x.dtype
-    out, ocode, ldo = _i8_dense_out(out, rows, w, out_dtype, x.device)
-    _same_device(x, ws[0], ws[1], out, w)
-    _i8_call("i8_linear", x.device, stream, _ptr(x), code, ld, rows, w.ref, _ptr(ws[0]),
-             _ptr(ws[1]), _ptr(out), ocode, ldo)
+    out, ocode, ldo = _i8_dense_out(out, rows, w, out_dtype, x, dev)
+    _i8_call("i8_linear", dev, stream, x.data_ptr(), code, ld, rows, w.ref, ws[0].data_ptr(),
+             ws[1].data_ptr(), out.data_ptr(), ocode, ldo)
     return out
 
 
@@ -657,24 +688,24 @@ def i8_moe_gemm(aq, as_, a_row, w: I8Experts, counts, basep, tile_m: int, mpad_m
     """mx4_moe_gemm in 8-bit integers over quantized rows (aq, as_) from i8_quantize: f32
     [mpad_max][N], or with MOE_ACT_SWIGLU_OAI (w built with glu) bf16 [mpad_max][N/2]."""
     torch = _torch()
-    rows = aq.shape[0]
-    _i8_out(aq, (rows, i8_pitch(w.K)), torch.int8, "aq")
-    _i8_out(as_, (rows,), torch.float32, "as")
+    rows, dev = aq.shape[0], aq.get_device()
+    _i8_weights(w, "w", dev)
+    _i8_check(aq, (rows, i8_pitch(w.K)), torch.int8, "aq", dev)
+    _i8_check(as_, (rows,), torch.float32, "as", dev)
     if a_row is not None:
-        _i8_out(a_row, (mpad_max,), torch.int32, "a_row")
-    _i8_out(counts, (w.E,), torch.int32, "counts")
-    _i8_out(basep, (w.E + 1,), torch.int32, "basep")
+        _i8_check(a_row, (mpad_max,), torch.int32, "a_row", dev)
+    _i8_check(counts, (w.E,), torch.int32, "counts", dev)
+    _i8_check(basep, (w.E + 1,), torch.int32, "basep", dev)
     swiglu = act == MOE_ACT_SWIGLU_OAI
     shape = (mpad_max, w.N // 2 if swiglu else w.N)
     dtype = torch.bfloat16 if swiglu else torch.float32
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=aq.device)
     else:
-        _i8_out(out, shape, dtype, "out")
-    _same_device(aq, as_, a_row, counts, basep, out, w)
-    _i8_call("i8_moe_gemm", aq.device, stream, _ptr(aq), _ptr(as_), _ptr(a_row), rows, w.ref,
-             _ptr(counts), _ptr(basep), tile_m, mpad_max, act, float(alpha), float(limit),
-             _ptr(out))
+        _i8_check(out, shape, dtype, "out", dev)
+    _i8_call("i8_moe_gemm", dev, stream, aq.data_ptr(), as_.data_ptr(),
+             None if a_row is None else a_row.data_ptr(), rows, w.ref, counts.data_ptr(),
+             basep.data_ptr(), tile_m, mpad_max, act, float(alpha), float(limit), out.data_ptr())
     return out
 
 
@@ -687,36 +718,40 @@ def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha:
     scratch of i8_row_buffers(T*k, F) (allocated if needed); concurrent calls need distinct
     scratch."""
     torch = _torch()
-    _check(logits, torch.float32, "logits")
-    _check(x, torch.bfloat16, "x")
-    if logits.dim() != 2 or tuple(x.shape) != (logits.shape[0], gate_up.K):
-        raise ValueError(f"logits {tuple(logits.shape)}, x {tuple(x.shape)}: expected [T][E] and "
-                         f"[T][{gate_up.K}]")
-    T, E = logits.shape
+    dev = x.get_device()
+    _i8_weights(gate_up, "gate_up", dev)
+    _i8_weights(down, "down", dev)
     D, F = gate_up.K, gate_up.N // 2
-    o = dict(out or {})
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected shape [T][E], got {tuple(logits.shape)}")
+    T, E = logits.shape
+    _i8_check(logits, (T, E), torch.float32, "logits", dev)
+    _i8_check(x, (T, D), torch.bfloat16, "x", dev)
+    o = dict(out) if out else {}
     if y_dtype is None:
         y_dtype = o["y"].dtype if "y" in o else torch.float32
-    shapes = {"ids": ((T, k), torch.int32), "w": ((T, k), torch.float32),
-              "h": ((T * k, F), torch.bfloat16), "y": ((T, D), y_dtype)}
-    if want_d or "d" in o:
-        shapes["d"] = ((T * k, D), torch.float32)
-    for key, (shape, dt) in shapes.items():
+    code = _i8_dtype(y_dtype, "y")
+    R = T * k
+    new = functools.partial(torch.empty, device=x.device)
+    for key, shape, dt in (("ids", (T, k), torch.int32), ("w", (T, k), torch.float32),
+                           ("h", (R, F), torch.bfloat16), ("y", (T, D), y_dtype),
+                           ("d", (R, D), torch.float32)):
         if key in o:
-            _i8_out(o[key], shape, dt, key)
-        else:
-            o[key] = torch.empty(shape, dtype=dt, device=x.device)
+            _i8_check(o[key], shape, dt, key, dev)
+        elif key != "d" or want_d:
+            o[key] = new(shape, dtype=dt)
+    q = s = None
     if ws is not None:
-        _i8_out(ws[0], (T * k, i8_pitch(F)), torch.int8, "ws[0]")
-        _i8_out(ws[1], (T * k,), torch.float32, "ws[1]")
-    elif T * k > 16 or F > 4096:
-        ws = i8_row_buffers(T * k, F, x.device)
-    else:
-        ws = (None, None)
-    _same_device(x, logits, gate_up, down, ws[0], ws[1], *(o[key] for key in shapes))
-    _i8_call("i8_moe_decode", x.device, stream, _ptr(logits), _ptr(x), T, E, k, gate_up.ref,
-             down.ref, float(alpha), float(limit), _ptr(o["ids"]), _ptr(o["w"]), _ptr(o["h"]),
-             _ptr(ws[0]), _ptr(ws[1]), _ptr(o.get("d")), _ptr(o["y"]), _i8_dtype(y_dtype, "y"))
+        _i8_check(ws[0], (R, i8_pitch(F)), torch.int8, "ws[0]", dev)
+        _i8_check(ws[1], (R,), torch.float32, "ws[1]", dev)
+    elif R > 16 or F > 4096:
+        ws = i8_row_buffers(R, F, x.device)
+    if ws is not None:
+        q, s = ws[0].data_ptr(), ws[1].data_ptr()
+    _i8_call("i8_moe_decode", dev, stream, logits.data_ptr(), x.data_ptr(), T, E, k, gate_up.ref,
+             down.ref, float(alpha), float(limit), o["ids"].data_ptr(), o["w"].data_ptr(),
+             o["h"].data_ptr(), q, s, o["d"].data_ptr() if "d" in o else None, o["y"].data_ptr(),
+             code)
     return o
 
 

@@ -185,49 +185,74 @@ __host__ __device__ __forceinline__ int i8_lds_pitch(int KP) {
 }
 __device__ __forceinline__ int i8_swizzle(int m, int off) { return off ^ (((m >> 1) & 7) << 4); }
 
-// A bf16 row spread over a wavefront: NV vectors of 8 values per lane, vector i of lane l holding
-// values 8 (64 i + l) .. + 7, zeros past the row. Rows of K % 8 == 0 values, 16-byte aligned.
-template <int NV>
+// A row spread over a wavefront: NV vectors of 8 values per lane, vector i of lane l holding values
+// 8 (64 i + l) .. + 7, zeros past the row. Rows of K % 8 == 0 values, 16-byte aligned.
+template <int NV, int DT = MOE_BF16>
 struct I8Row {
-  uint4 v[NV];
-  __device__ __forceinline__ void load(const uint16_t* __restrict__ row, int K) {
+  static constexpr int kWords = DT == MOE_F32 ? 8 : 4;   // 32-bit words of a vector
+  uint32_t v[NV][kWords];
+  __device__ __forceinline__ void load(const void* __restrict__ row, int K) {
     const int lane = (int)(threadIdx.x & 63);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int u = i * kWave + lane;
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (u * 8 < K) v[i] = *reinterpret_cast<const uint4*>(row + u * 8);
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) v[i][j] = 0u;
+      if (u * 8 < K) {
+        const uint4* p = (const uint4*)row + u * (kWords / 4);
+#pragma unroll
+        for (int j = 0; j < kWords / 4; ++j) {
+          const uint4 t = p[j];
+          v[i][4 * j] = t.x;
+          v[i][4 * j + 1] = t.y;
+          v[i][4 * j + 2] = t.z;
+          v[i][4 * j + 3] = t.w;
+        }
+      }
     }
   }
-  // Largest magnitude as an f32 pattern (a bf16 pattern shifted), the same in every lane: two
-  // values a step as unsigned halves (for patterns without sign the integer order is the float's)
+  // Largest magnitude as an f32 pattern, the same in every lane. Patterns without their sign
+  // order as the values do, NaN above infinity: 16-bit ones go two a step as unsigned halves.
   __device__ __forceinline__ uint32_t largest() const {
-    typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
-    u16x2_t m = {0, 0};
-    auto take = [&](uint32_t w) {
-      w &= 0x7FFF7FFFu;
-      u16x2_t t;
-      __builtin_memcpy(&t, &w, sizeof(t));
-      m = __builtin_elementwise_max(m, t);
-    };
+    if constexpr (DT == MOE_F32) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      take(v[i].x);
-      take(v[i].y);
-      take(v[i].z);
-      take(v[i].w);
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) m = max(m, v[i][j] & 0x7FFFFFFFu);
+      return wave_umax(m);
+    } else {
+      typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+      u16x2_t m = {0, 0};
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          const uint32_t w = v[i][j] & 0x7FFF7FFFu;
+          u16x2_t t;
+          __builtin_memcpy(&t, &w, sizeof(t));
+          m = __builtin_elementwise_max(m, t);
+        }
+      const uint32_t top = wave_umax(max((uint32_t)m[0], (uint32_t)m[1]));
+      if constexpr (DT == MOE_BF16) return top << 16;
+      return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
     }
-    return wave_umax(max((uint32_t)m[0], (uint32_t)m[1]) << 16);
   }
   __device__ __forceinline__ uint2 codes(const I8Quant& z, int i) const {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     float f[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < kWords; ++j) {
+      if constexpr (DT == MOE_F32) {
+        f[j] = __uint_as_float(v[i][j]);
+      } else if constexpr (DT == MOE_F16) {
+        f[2 * j] = __half2float(__ushort_as_half((unsigned short)(v[i][j] & 0xFFFFu)));
+        f[2 * j + 1] = __half2float(__ushort_as_half((unsigned short)(v[i][j] >> 16)));
+      } else {
+        f[2 * j] = __uint_as_float(v[i][j] << 16);
+        f[2 * j + 1] = __uint_as_float(v[i][j] & 0xFFFF0000u);
+      }
     }
-    return codes8<MOE_BF16>(z, f);
+    return codes8<DT>(z, f);
   }
   // Codes of the vectors i with i % parts == part (parts a power of two) into row m of an LDS
   // image (pitch LP)
@@ -256,24 +281,78 @@ struct I8Row {
   }
 };
 
-// The same for any row, read twice: its scale, and its codes into row m of an LDS image.
-__device__ __forceinline__ float i8_row_to_lds(const uint16_t* __restrict__ row, int K, uint8_t* lds,
-                                               int m, int LP, int KP) {
+// The same for any row from element r0 of x on, read twice: its scale, and its codes into row m of
+// an LDS image.
+template <int DT>
+__device__ __forceinline__ float i8_row_to_lds(const void* __restrict__ x, int64_t r0, int K,
+                                               uint8_t* lds, int m, int LP, int KP) {
   const int lane = (int)(threadIdx.x & 63);
   uint32_t top = 0;
   for (int u = lane; u * 8 < K; u += kWave) {
     float t[8];
-    load8<MOE_BF16, false>(row, u * 8, K - u * 8, t);
+    load8<DT, false>(x, r0 + u * 8, K - u * 8, t);
     top = max_abs8(t, top);
   }
   const I8Quant z(wave_umax(top));
   for (int u = lane; u * 8 < KP; u += kWave) {
     float t[8];
-    load8<MOE_BF16, false>(row, u * 8, K - u * 8, t);
+    load8<DT, false>(x, r0 + u * 8, K - u * 8, t);
     *reinterpret_cast<uint2*>(lds + m * LP + i8_swizzle(m, (u * 8) & ~15) + ((u * 8) & 8)) =
-        codes8<MOE_BF16>(z, t);
+        codes8<DT>(z, t);
   }
   return z.s;
 }
+
+// A barrier for what was written to LDS: loads from memory stay in flight (__syncthreads() would
+// wait for all of them).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A run of n <= NR chunks of one weight tile: where its first chunk starts in an expert's stack.
+// A run of no chunks reads nothing (its loads are out of range and give zeros).
+struct I8Run {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off, step;
+  int n;
+};
+
+// NR chunks of a run in registers, refilled one by one from the run after it as they are used, so
+// that a wavefront has NR KB in flight from its first run to its last. Buffer loads: the
+// resource is one expert's stack and the chunk a scalar offset, so that a load takes no address
+// registers. Chunks past the end of a run are zeros, and so are their products.
+template <int NR>
+struct I8Ring {
+  u32x4_t v[NR];
+  __device__ __forceinline__ void load(int i, const I8Run& run) {
+    const uint32_t lane16 = (threadIdx.x & 63) * 16;
+    v[i] = buf_load16_nt(run.r, i < run.n ? lane16 : kOOB, i < run.n ? run.off + (uint32_t)i * run.step : 0u);
+  }
+  __device__ __forceinline__ void fill(const I8Run& run) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) load(i, run);
+  }
+  // acc += the products of the run held with the B operands from LDS row bp (its m-th row), the
+  // run's first chunk being c0; the ring is refilled from `next`
+  __device__ __forceinline__ void take(const uint8_t* bp, int m, int c0, int clast, const I8Run& next,
+                                       i32x4_t& acc, i32x4_t& acc1) {
+    const int g16 = ((int)(threadIdx.x & 63) >> 4) * 16;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const i32x4_t b = *reinterpret_cast<const i32x4_t*>(
+          bp + i8_swizzle(m, min(c0 + i, clast) * kI8Chunk + g16));
+      i32x4_t a;
+      __builtin_memcpy(&a, &v[i], sizeof(a));
+      if (i & 1)
+        acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc1, 0, 0, 0);
+      else
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
+      load(i, next);
+      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few B operands at a time
+    }
+  }
+};
 
 }  // namespace moe

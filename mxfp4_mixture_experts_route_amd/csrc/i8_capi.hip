@@ -7,6 +7,10 @@ int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, i
                        int64_t rows, int64_t mpad, int act, float alpha, float limit, void* out,
                        int out_dt, int64_t ld_out, hipStream_t stream);
 
+bool moe_i8_few(int64_t rows, const i8_experts* w);
+int moe_launch_i8_few(const void* x, int x_dt, int64_t ld, int rows, const i8_experts* w, void* out,
+                      int out_dt, int64_t ld_out, hipStream_t stream);
+
 namespace {
 
 bool known_dtype(int dt) { return dt == MOE_BF16 || dt == MOE_F16 || dt == MOE_F32; }
@@ -76,6 +80,9 @@ extern "C" int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows,
   st = check_align(q_ws, s_ws, w, out, out_dtype);
   if (st != MOE_OK) return st;
   if (((uintptr_t)x) & (elem_size(x_dtype) - 1)) return MOE_EALIGN;
+  if (moe_i8_few(rows, w))
+    return moe_launch_i8_few(x, x_dtype, ld, (int)rows, w, out, out_dtype, ld_out,
+                             (hipStream_t)stream);
   st = i8_quantize(x, x_dtype, ld, nullptr, rows, w->K, q_ws, s_ws, stream);
   if (st != MOE_OK) return st;
   return moe_launch_i8_gemm(q_ws, s_ws, nullptr, rows, w, nullptr, nullptr, rows, rows,

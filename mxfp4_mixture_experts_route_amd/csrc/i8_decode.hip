@@ -32,14 +32,6 @@ constexpr int kI8LdsRows = 16;      // h rows that launch 2 quantizes itself
 constexpr int kI8DecVec = 8;        // row vectors per lane held in registers (K <= 4096)
 constexpr size_t kI8DecMaxLds = 140 * 1024;   // quantized rows in LDS
 
-// A barrier for what was written to LDS: loads from memory stay in flight (__syncthreads() would
-// wait for all of them).
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // The j-th expert (ascending) of those set in a bitmap of E <= 1024 bits, or -1; every lane of
 // the calling wavefront gets it.
 __device__ __forceinline__ int nth_expert(const uint32_t* bits, int j) {
@@ -76,51 +68,6 @@ __device__ __forceinline__ int rows_of_expert(const int* sid, int R, int e, int*
   }
   return n;
 }
-
-// A run of n <= NR chunks of 16 weight rows: where its first chunk starts in an expert's stack.
-// A run of no chunks reads nothing (its loads are out of range and give zeros).
-struct I8Run {
-  __amdgpu_buffer_rsrc_t r;
-  uint32_t off, step;
-  int n;
-};
-
-// NR chunks of a run in registers, refilled one by one from the run after it as they are used, so
-// that a wavefront has NR KB in flight from its first run to its last. Buffer loads: the
-// resource is one expert's stack and the chunk a scalar offset, so that a load takes no address
-// registers. Chunks past the end of a run are zeros, and so are their products.
-template <int NR>
-struct I8Ring {
-  u32x4_t v[NR];
-  uint32_t voff;   // the lane's place in a chunk: its number times 16 where the rows are a tile
-  __device__ __forceinline__ explicit I8Ring(uint32_t lane_off) : voff(lane_off) {}
-  __device__ __forceinline__ void load(int i, const I8Run& run) {
-    v[i] = buf_load16_nt(run.r, i < run.n ? voff : kOOB, i < run.n ? run.off + (uint32_t)i * run.step : 0u);
-  }
-  __device__ __forceinline__ void fill(const I8Run& run) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i) load(i, run);
-  }
-  // acc += the products of the run held with the B operands from LDS row bp (its m-th row), the
-  // run's first chunk being c0; the ring is refilled from `next`
-  __device__ __forceinline__ void take(const uint8_t* bp, int m, int c0, int clast, const I8Run& next,
-                                       i32x4_t& acc, i32x4_t& acc1) {
-    const int g16 = ((int)(threadIdx.x & 63) >> 4) * 16;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const i32x4_t b = *reinterpret_cast<const i32x4_t*>(
-          bp + i8_swizzle(m, min(c0 + i, clast) * kI8Chunk + g16));
-      i32x4_t a;
-      __builtin_memcpy(&a, &v[i], sizeof(a));
-      if (i & 1)
-        acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc1, 0, 0, 0);
-      else
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
-      load(i, next);
-      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few B operands at a time
-    }
-  }
-};
 
 // ---- one token -------------------------------------------------------------------------------
 // The picks of one token are k different experts with one row each, which is the same row (launch
@@ -188,7 +135,7 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   auto run = [&](int c0) {
     return I8Run{rw, ((uint32_t)(cb + c0) * NT + tile) * kI8TileBytes, step, len - c0};
   };
-  I8Ring<kI8UpRing> ring(lane * 16);
+  I8Ring<kI8UpRing> ring;
   ring.fill(run(0));
   const int F = N >> 1, n = unit * 16 + col;
   const int64_t cg = (int64_t)e * N + min(n, F - 1);
@@ -219,41 +166,9 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   }
 }
 
-// Channels of a workgroup of launch 2. One CU takes in about 26 KB/us of weights (11 B a clock),
-// so the launch lasts as long as the CU with the most channels: with 16 each, 2880 channels keep
-// 180 of the 256 CUs busy, with 12 each 240 (16 tokens: 55.6 -> SPAN16 us). Fewer than 16 channels
-// leave rows of the MFMA operand empty, which costs nothing here.
-inline int down_span(int D) {
-  int best = 16, most = 0x7FFFFFFF;
-  for (int span = 16; span >= 4; span -= 4) {
-    const int units = (D + span - 1) / span, crit = (units + 255) / 256 * span;
-    if (crit < most) {
-      most = crit;
-      best = span;
-    }
-  }
-  return best;
-}
-
-// The lane's place in a chunk of the weights: row lane % 16 of the span's, from channel n0 on,
-// may lie in two tiles; lanes past the span or the last channel read nothing.
-__device__ __forceinline__ uint32_t span_lane(int n0, int span, int D) {
-  const int lane = (int)(threadIdx.x & 63), r = lane & 15, n = n0 + r;
-  return r < span && n < D
-             ? (uint32_t)((n >> 4) * kI8TileBytes + (lane >> 4) * 256 + (n & 15) * 16)
-             : kOOB;
-}
-
-// Neighbouring units share cache lines where a span is not a whole tile: they go to one XCD
-// (workgroups are dealt to the 8 XCDs round robin).
-__device__ __forceinline__ int xcd_unit(int units) {
-  const int per = (units + 7) >> 3, x = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3;
-  return i < per && x * per + i < units ? x * per + i : -1;
-}
-
-// Launch 2: a workgroup owns `span` channels; wavefronts {slots} x {parts of K}.
+// Launch 2: a workgroup owns 16 channels; wavefronts {slots} x {parts of K}.
 __global__ void __launch_bounds__(1024)
-i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts, int span, int units,
+i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
                    const int32_t* __restrict__ ids, const float* __restrict__ w,
                    const int8_t* __restrict__ wq, const float* __restrict__ wsc,
                    const float* __restrict__ bias, int D, int F, float* __restrict__ d,
@@ -263,8 +178,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts, int 
   __shared__ float dv_s[MOE_DECODE_MAX_K][kI8TileRows];
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int unit = xcd_unit(units), slot = wave / parts, part = wave - slot * parts;
-  if (unit < 0) return;
+  const int unit = (int)blockIdx.x, slot = wave / parts, part = wave - slot * parts;
   int e = ids[slot];
   const float wt = w[slot];
   __builtin_amdgcn_sched_barrier(0);   // the id comes first
@@ -277,11 +191,11 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts, int 
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step);
   auto run = [&](int c0) {
-    return I8Run{rw, (uint32_t)(cb + c0) * step, step, len - c0};
+    return I8Run{rw, ((uint32_t)(cb + c0) * NT + unit) * kI8TileBytes, step, len - c0};
   };
-  I8Ring<kI8OneRing> ring(span_lane(unit * span, span, D));
+  I8Ring<kI8OneRing> ring;
   ring.fill(run(0));
-  const int n = unit * span + col;
+  const int n = unit * 16 + col;
   const int64_t cg = (int64_t)e * D + min(n, D - 1);
   float sc = 0.0f, bi = 0.0f;
   if (part == 0) {
@@ -299,7 +213,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts, int 
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][4 * g + i] = acc[i];
   lds_barrier();
-  if (part == 0 && lane < span) {
+  if (part == 0 && lane < kI8TileRows) {
     int sum = 0;
     for (int p = 0; p < parts; ++p) sum += red[wave + p][lane];
     const float dv = fmaf((float)sum, z.s * sc, bi);
@@ -308,7 +222,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts, int 
     red[wave][lane] = __float_as_int(dv);
   }
   lds_barrier();
-  if (tid < span && n < D) {
+  if (tid < kI8TileRows && n < D) {
     float yv = 0.0f;
     for (int s = 0; s < k; ++s) yv = fmaf(dv_s[s][tid], __int_as_float(red[s * parts][tid]), yv);
     store_elem(y, n, yv, y_dt);
@@ -404,11 +318,11 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     return I8Run{rw, ((uint32_t)(cb + c0) * NT + half + unit) * kI8TileBytes, step,
                  unit < uend ? len - c0 : 0};
   };
-  I8Ring<kI8UpRing> ring(lane * 16);
+  I8Ring<kI8UpRing> ring;
   I8Row<kI8DecVec> xr;
   if (!fast) {
     for (int m = wave; m < cnt; m += kWaves) {
-      const float s = i8_row_to_lds(x + (int64_t)(list[m] / k) * K, K, rowsq, m, LP, KP);
+      const float s = i8_row_to_lds<MOE_BF16>(x, (int64_t)(list[m] / k) * K, K, rowsq, m, LP, KP);
       if (lane == 0) sx[m] = s;
     }
     ring.fill(run(ubase, 0));
@@ -512,8 +426,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
                       const float* __restrict__ hs, int T, int E, int k,
                       const int32_t* __restrict__ ids, const float* __restrict__ w,
                       const int8_t* __restrict__ wq, const float* __restrict__ wsc,
-                      const float* __restrict__ bias, int D, int F, int fast, int span, int units,
-                      float* __restrict__ d, void* __restrict__ y, int y_dt) {
+                      const float* __restrict__ bias, int D, int F, int fast, float* __restrict__ d, void* __restrict__ y, int y_dt) {
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // R quantized rows, or none
   constexpr int kWaves = kI8DownThreads / kWave;
   constexpr int NR = ROWS ? kI8RowsRing : kI8DownRing;
@@ -523,8 +436,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   __shared__ int acc_s[kI8DecMaxR][kI8TileRows];     // sums of each routed row, then its d (f32)
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int R = T * k, unit = xcd_unit(units);
-  if (unit < 0) return;
+  const int R = T * k, unit = (int)blockIdx.x;
   const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = FP / kI8Chunk, NT = i8_tiles(D, 0);
 
   for (int i = tid; i < R * kI8TileRows; i += kI8DownThreads) (&acc_s[0][0])[i] = 0;
@@ -532,15 +444,15 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   p.build(ids, w, R, E);
   const int picked = __builtin_amdgcn_readfirstlane(p.picked);
 
-  // an item is one picked expert's rows of the span over a segment of K
+  // an item is one picked expert's tile over a segment of K
   const int segs = (C + NR - 1) / NR, items = picked * segs;
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
   auto run = [&](int it) {
     const int jx = it / segs, seg = it - jx * segs;
     const int cb = C * seg / segs, ce = C * (seg + 1) / segs;
     const int e = it < items ? __builtin_amdgcn_readfirstlane(p.ex[jx]) : 0;
-    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step), (uint32_t)cb * step, step,
-                 it < items ? ce - cb : 0};
+    return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step),
+                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, it < items ? ce - cb : 0};
   };
   // ROWS: the lane's row and piece of the item's activations, behind which its segment's chunks lie
   auto rows = [&](int it) {
@@ -548,7 +460,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
     const int m = p.start[jx] + min(col, p.start[jx + 1] - p.start[jx] - 1);
     return (uint32_t)(p.ord[m] * FP + g * 16);
   };
-  I8Ring<NR> ring(span_lane(unit * span, span, D));
+  I8Ring<NR> ring;
   u32x4_t bv[ROWS ? NR : 1];
   const __amdgpu_buffer_rsrc_t rh = make_rsrc(hq, ROWS ? (uint32_t)(R * FP) : 0u);
   if constexpr (ROWS) {
@@ -573,7 +485,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
       }
     } else {
       for (int m = wave; m < R; m += kWaves) {
-        const float s = i8_row_to_lds(h + (int64_t)p.ord[m] * F, F, rowsq, m, LP, FP);
+        const float s = i8_row_to_lds<MOE_BF16>(h, (int64_t)p.ord[m] * F, F, rowsq, m, LP, FP);
         if (lane == 0) sh[p.ord[m]] = s;
       }
       ring.fill(run(wave));
@@ -582,7 +494,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   }
 
   // scales and biases of the sums this thread turns into d: channel tid % 16 of rows tid / 16 + 32 i
-  const int jj = tid & 15, n = jj < span ? unit * span + jj : D;   // D: none
+  const int jj = tid & 15, n = unit * 16 + jj;
   float dsc[kSums], dbi[kSums];
 #pragma unroll
   for (int i = 0; i < kSums; ++i) {
@@ -694,7 +606,6 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
   const hipStream_t st = (hipStream_t)stream;
   const int fast1 = D % 8 == 0 && D <= moe::kI8DecVec * 8 * moe::kWave;
   const int fast2 = F % 8 == 0 && F <= moe::kI8DecVec * 8 * moe::kWave;
-  const int span = moe::down_span(D), dunits = (D + span - 1) / span;
   if (T == 1 && fast1 && fast2) {
     const int Cd = moe::i8_pitch(D) / moe::kI8Chunk, Cf = moe::i8_pitch(F) / moe::kI8Chunk;
     // launch 2: 16 wavefronts, or as many as there are slots and chunks for
@@ -704,10 +615,10 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
                 (size_t)(4 * ((Cd + 1) / 2) * moe::kI8Chunk), st, logits, x, E, k, w_gu->q, w_gu->s,
                 w_gu->bias, N, D, alpha, limit, units, ids, w, h);
     if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
-    moe::launch(moe::i8_one_down_kernel, dim3((unsigned)((dunits + 7) / 8 * 8)),
+    moe::launch(moe::i8_one_down_kernel, dim3((unsigned)moe::i8_tiles(D, 0)),
                 dim3((unsigned)(64 * k * parts)),
-                (size_t)(k * parts * ((Cf + parts - 1) / parts) * moe::kI8Chunk), st, h, E, k, parts,
-                span, dunits, ids, w, w_dn->q, w_dn->s, w_dn->bias, D, F, d, y, y_dtype);
+                (size_t)(k * parts * ((Cf + parts - 1) / parts) * moe::kI8Chunk), st, h, E, k, parts, ids,
+                w, w_dn->q, w_dn->s, w_dn->bias, D, F, d, y, y_dtype);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
   }
   const int picks = R < E ? R : E;
@@ -728,11 +639,11 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
               dim3(moe::kI8DecThreads), lds1, st, logits, x, (int)T, E, k, w_gu->q, w_gu->s,
               w_gu->bias, N, D, alpha, limit, units, upw, fast1, ids, w, h);
   if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
-  const dim3 grid2((unsigned)((dunits + 7) / 8 * 8));
+  const dim3 grid2((unsigned)moe::i8_tiles(D, 0));
   if (own_rows) {
     moe::launch(moe::i8_decode_down_kernel<false>, grid2, dim3(moe::kI8DownThreads), lds2, st, h,
                 (const int8_t*)nullptr, (const float*)nullptr, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
-                w_dn->bias, D, F, fast2, span, dunits, d, y, y_dtype);
+                w_dn->bias, D, F, fast2, d, y, y_dtype);
   } else {
     // every workgroup of launch 2 would quantize every row, some 2 us for 8 of them: more than 16
     // rows are quantized once, by a launch of its own
@@ -740,7 +651,7 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
     if (qs != MOE_OK) return qs;
     moe::launch(moe::i8_decode_down_kernel<true>, grid2, dim3(moe::kI8DownThreads), 0, st, h,
                 (const int8_t*)q_ws, (const float*)s_ws, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
-                w_dn->bias, D, F, fast2, span, dunits, d, y, y_dtype);
+                w_dn->bias, D, F, fast2, d, y, y_dtype);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }
