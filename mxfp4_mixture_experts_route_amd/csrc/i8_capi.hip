@@ -60,6 +60,7 @@ extern "C" int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_r
   if (tile_m < 1 || tile_m > MOE_MAX_TILE_M || mpad_max > 0x7FFFFFFFLL || a_rows > 0x7FFFFFFFLL)
     return MOE_ESHAPE;
   if (!a_row && a_rows < mpad_max) return MOE_ESHAPE;
+  if (a_rows * moe::i8_pitch(w->K) >= (int64_t)1 << 32) return MOE_ESHAPE;   // rows within 4 GB
   const bool glu = act == MOE_ACT_SWIGLU_OAI;
   const int out_dt = glu ? MOE_BF16 : MOE_F32;
   st = check_align(aq, as, w, out, out_dt);

@@ -21,59 +21,66 @@ namespace moe {
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
 
-template <int BM_, int BN_, int WM_, int WN_, int NST_>
+// WK > 1: WK wavefronts split K, each with a ring of its own, and their sums meet in LDS at the end;
+// there is no barrier in the K loop.
+template <int BM_, int BN_, int WM_, int WN_, int NST_, int WK_ = 1>
 struct I8Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
-  static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, WK = WK_;
+  static constexpr int kWaves = WM * WN, kThreads = kWaves * WK * kWave;   // (waves of a group)
   static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;      // 32x32 blocks per wavefront
   static constexpr int kOps = (BM + BN) / 16;                     // 1 KB copies per chunk
   static constexpr int kOpsW = (kOps + kWaves - 1) / kWaves;      // of a wavefront
   static constexpr int kStage = (BM + BN) * kI8Chunk;
-  static constexpr int kLds = NST * kStage + (BM + BN) * 8;       // + what the epilogue needs per row and channel
+  static constexpr int kRing = WK * NST * kStage;
+  static constexpr int kRed = WK > 1 ? WK * BM * BN * 4 : 0;   // sums of the groups, where the rings were
+  static constexpr int kLds = kRing + (BM + BN) * 8;   // + what the epilogue needs per row and channel
   static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "whole blocks");
-  static_assert((NST - 1) * kOpsW <= 63, "vmcnt range");
+  static_assert(NST * kOpsW <= 63, "vmcnt range");
+  static_assert(WK == 1 || kWaves == 1, "groups of one wavefront");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
-// The work item of a routed launch: (expert, block of rows) number `blk` of those that hold live
-// rows, in expert order; every wavefront computes it for itself. Returns the number of all such
-// blocks; e < 0 where blk is past them.
+// The row blocks of a routed launch: the experts' blocks of BM rows, numbered in expert order.
+// Lane l of every wavefront holds the experts l * per .. of the list.
 template <int BM>
-__device__ __forceinline__ int routed_block(const int32_t* __restrict__ counts, int E, int blk,
-                                            int& e, int& m) {
-  const int lane = (int)(threadIdx.x & 63);
-  const int per = (E + kWave - 1) / kWave;
-  const int e0 = lane * per;
-  int mine = 0;
-  for (int i = 0; i < per; ++i)
-    if (e0 + i < E) mine += (max(counts[e0 + i], 0) + BM - 1) / BM;
-  int upto = mine;
+struct I8Blocks {
+  int per, upto, mine, total;   // experts a lane, blocks up to and of this lane's, all blocks
+
+  __device__ __forceinline__ int of(const int32_t* __restrict__ counts, int e, int E) const {
+    return e < E ? (max(counts[e], 0) + BM - 1) / BM : 0;
+  }
+  __device__ __forceinline__ I8Blocks(const int32_t* __restrict__ counts, int E) {
+    const int lane = (int)(threadIdx.x & 63);
+    per = (E + kWave - 1) / kWave;
+    mine = 0;
+    for (int i = 0; i < per; ++i) mine += of(counts, lane * per + i, E);
+    upto = mine;
 #pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int u = __shfl_up(upto, o);
-    if (lane >= o) upto += u;
-  }
-  const int total = __shfl(upto, kWave - 1);
-  const bool here = blk >= upto - mine && blk < upto;
-  int fe = -1, fm = 0;
-  if (here) {
-    int left = blk - (upto - mine);
-    for (int i = 0; i < per; ++i) {
-      const int b = e0 + i < E ? (max(counts[e0 + i], 0) + BM - 1) / BM : 0;
-      if (left < b) {
-        fe = e0 + i;
-        fm = left;
-        break;
-      }
-      left -= b;
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int u = __shfl_up(upto, o);
+      if (lane >= o) upto += u;
     }
+    total = __builtin_amdgcn_readlane(upto, kWave - 1);
   }
-  const uint64_t who = __ballot(here);
-  const int src = who ? __ffsll((unsigned long long)who) - 1 : 0;
-  e = __shfl(fe, src);
-  m = __shfl(fm, src);
-  return total;
-}
+  // Expert of block number blk (< total), its block there, the number of its blocks.
+  __device__ __forceinline__ void find(const int32_t* __restrict__ counts, int E, int blk, int& e,
+                                       int& m, int& n) const {
+    const int lane = (int)(threadIdx.x & 63);
+    const bool here = blk >= upto - mine && blk < upto;
+    int left = blk - (upto - mine), fe = lane, fn = mine;
+    if (per > 1 && here)
+      for (int i = 0; i < per; ++i) {
+        fe = lane * per + i;
+        fn = of(counts, fe, E);
+        if (left < fn) break;
+        left -= fn;
+      }
+    const int src = __ffsll((unsigned long long)__ballot(here)) - 1;
+    e = __builtin_amdgcn_readlane(fe, src);
+    m = __builtin_amdgcn_readlane(left, src);
+    n = __builtin_amdgcn_readlane(fn, src);
+  }
+};
 
 template <class TL, bool GLU, bool ROUTED, int OUT>
 __global__ void __launch_bounds__(TL::kThreads)
@@ -87,7 +94,8 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   constexpr int BM = TL::BM, BN = TL::BN, NST = TL::NST, FM = TL::FM, FN = TL::FN;
   constexpr int kUnits = GLU ? BN / 32 : BN / 16;   // 16-channel units of the workgroup
   const int tid = (int)threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = TL::WK > 1 ? 0 : wid, part = TL::WK > 1 ? wid : 0;
 
   // 1. the item: workgroups are dealt to the 8 XCDs round robin, so item numbers are dealt in 8
   // contiguous shares, and an XCD's L2 sees neighbouring items
@@ -95,17 +103,15 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   {
     const int x = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3;
     if constexpr (ROUTED) {
-      int m0;
-      const int blocks = routed_block<BM>(counts, E, 0, e, m0);
-      const int total = blocks * nblocks, per = (total + 7) >> 3;
+      const I8Blocks<BM> blocks(counts, E);
+      const int total = blocks.total * nblocks, per = (total + 7) >> 3;
       const int item = x * per + i;
       if (i >= per || item >= total) return;
       // items of an expert are neighbours, its row blocks the nearest (they share the weights)
       const int blk0 = item / nblocks;
-      routed_block<BM>(counts, E, blk0, e, m0);
-      const int first = blk0 - m0;                              // the expert's first block
-      const int eb = ((int)counts[e] + BM - 1) / BM;            // its number of blocks
-      const int in = item - first * nblocks;
+      int m0, eb;
+      blocks.find(counts, E, blk0, e, m0, eb);
+      const int in = item - (blk0 - m0) * nblocks;
       nb = in / eb;
       mb = in - nb * eb;
     } else {
@@ -132,60 +138,59 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   const int live = (int)min((int64_t)BM, count - r0);
   if (live <= 0) return;
 
-  // 2. source row and scale of every row of the block, scale and bias of every channel
+  // 2. source row of every row of the block
   const int NT = i8_tiles(N, glu), HT = i8_half_tiles(N, glu);
   const int u0 = nb * kUnits;
-  int* const src_s = reinterpret_cast<int*>(lds + NST * TL::kStage);
+  int* const src_s = reinterpret_cast<int*>(lds + TL::kRing);
   float* const scale_s = reinterpret_cast<float*>(src_s + BM);
   float* const wsc_s = scale_s + BM;
   float* const bias_s = wsc_s + BN;
   for (int m = tid; m < BM; m += TL::kThreads) {
     int64_t src = -1;
     if (m < live) {
-      src = a_row ? (int64_t)a_row[base + r0 + m] : base + r0 + m;
+      src = ROUTED && a_row ? (int64_t)a_row[base + r0 + m] : base + r0 + m;
       if ((uint64_t)src >= (uint64_t)a_rows) src = -1;   // such a row is not stored
     }
     src_s[m] = (int)src;
-    scale_s[m] = src >= 0 ? as[src] : 0.0f;
-  }
-  for (int j = tid; j < BN; j += TL::kThreads) {
-    const int u = j >> 4;   // the unit, or of SwiGLU the gate or up tile of it
-    const int t = GLU ? ((u & 1) ? HT : 0) + min(u0 + (u >> 1), HT - 1) : min(u0 + u, NT - 1);
-    const int n = i8_channel(t, j & 15, N, glu);
-    wsc_s[j] = n >= 0 ? wsc[(int64_t)e * N + n] : 0.0f;
-    bias_s[j] = n >= 0 && bias ? bias[(int64_t)e * N + n] : 0.0f;
   }
   __syncthreads();
 
   // 3. copies of a chunk: operation j < BN / 16 is weight tile j, the others 16 rows each
-  const int KP = i8_pitch(K), C = KP / kI8Chunk;
-  const int8_t* src[TL::kOpsW];
-  int64_t step[TL::kOpsW];
-  int dst[TL::kOpsW];
+  const int KP = i8_pitch(K), CK = KP / kI8Chunk;
+  const int cb = CK * part / TL::WK, C = CK * (part + 1) / TL::WK - cb;   // this group's chunks
+  uint8_t* const ring = lds + part * NST * TL::kStage;
+  // operation number i of this wavefront; a surplus one repeats the last (the same bytes to the
+  // same place)
+  auto op = [&](int i) { return min(wave + i * TL::kWaves, TL::kOps - 1); };
+  // each operation: a 64-bit scalar address that steps through the chunks and a 32-bit offset per
+  // lane (the rows of a routed product lie within 4 GB, a dense one starts at its own rows)
+  const int64_t wstep = (int64_t)NT * kI8TileBytes;
+  const int8_t* wbase = wq + ((int64_t)e * CK + cb) * wstep;
+  const int8_t* abase = a + (ROUTED ? 0 : r0 * KP) + cb * kI8Chunk;
+  const int first = ROUTED ? 0 : (int)r0;
+  uint32_t voff[TL::kOpsW];
 #pragma unroll
   for (int i = 0; i < TL::kOpsW; ++i) {
-    // a surplus operation repeats the last one (the same bytes to the same place)
-    const int j = min(wave + i * TL::kWaves, TL::kOps - 1);
-    dst[i] = j * 1024;
+    const int j = op(i);
     if (j < BN / 16) {
       // tiles past the last one repeat it; their channels are not stored
       const int t = GLU ? (j & 1) * HT + min(u0 + (j >> 1), HT - 1) : min(u0 + j, NT - 1);
-      src[i] = wq + ((int64_t)e * C * NT + t) * kI8TileBytes + lane * 16;
-      step[i] = (int64_t)NT * kI8TileBytes;
+      voff[i] = (uint32_t)t * kI8TileBytes + lane * 16;
     } else {
       const int m = (j - BN / 16) * 16 + (lane >> 2);
       const int piece = (lane & 3) ^ ((m >> 2) & 3);
-      src[i] = a + (int64_t)max(src_s[m], 0) * KP + piece * 16;
-      step[i] = kI8Chunk;
+      voff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
     }
   }
   auto issue = [&](int slot) {
 #pragma unroll
     for (int i = 0; i < TL::kOpsW; ++i) {
-      __builtin_amdgcn_global_load_lds((gptr_t)src[i],
-                                       (lptr_t)(lds + slot * TL::kStage + dst[i]), 16, 0, 0);
-      src[i] += step[i];
+      const int j = op(i);
+      __builtin_amdgcn_global_load_lds((gptr_t)((j < BN / 16 ? wbase : abase) + voff[i]),
+                                       (lptr_t)(ring + slot * TL::kStage + j * 1024), 16, 0, 0);
     }
+    wbase += wstep;
+    abase += kI8Chunk;
   };
 
   // 4. the K loop
@@ -204,95 +209,215 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][m][i] = 0;
 
+  // The operands of each half chunk (32 of K) are read while the products of the half before run:
+  // read right before their products, 1 to 2 wavefronts a SIMD waited for LDS in every half
+  i32x4_t wv[2][FN], av[2][FM];
+  auto read = [&](int h, const uint8_t* st) {
 #pragma unroll
-  for (int s = 0; s < NST - 1; ++s)
-    if (s < C) issue(s);
-  int slot = 0, fill = NST - 1;
-  for (int c = 0; c < C; ++c) {
-    // this wavefront's copies of chunk c have landed (those of the chunks after it may be in
-    // flight); the barrier says so for every wavefront, and that chunk c - 1 has been read
+    for (int f = 0; f < FN; ++f)
+      wv[h][f] = *reinterpret_cast<const i32x4_t*>(st + wo + f * 2048 + h * 512);
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+      av[h][m] = *reinterpret_cast<const i32x4_t*>(st + ao + m * 32 * kI8Chunk + (p0 ^ (h * 32)));
     __builtin_amdgcn_sched_barrier(0);
-    if (c + NST - 1 <= C)
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsW));
-    else
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    if (c + NST - 1 < C) issue(fill);
-    fill = fill == NST - 1 ? 0 : fill + 1;
-    const uint8_t* st = lds + slot * TL::kStage;
-    slot = slot == NST - 1 ? 0 : slot + 1;
+  };
+  auto multiply = [&](int h) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      i32x4_t wv[FN], av[FM];
-#pragma unroll
-      for (int f = 0; f < FN; ++f)
-        wv[f] = *reinterpret_cast<const i32x4_t*>(st + wo + f * 2048 + ks * 512);
+    for (int f = 0; f < FN; ++f)
 #pragma unroll
       for (int m = 0; m < FM; ++m)
-        av[m] = *reinterpret_cast<const i32x4_t*>(st + ao + m * 32 * kI8Chunk + (p0 ^ (ks * 32)));
+        acc[f][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[h][f], av[h][m], acc[f][m], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int s = 0; s < NST; ++s)
+    if (s < C) issue(s);
+  __builtin_amdgcn_sched_barrier(0);
+  // what the epilogue needs goes out behind the first copies: the scale of a row, scale and bias
+  // of a channel, up to kExtra values a thread
+  constexpr int kRowsT = (BM + TL::kThreads - 1) / TL::kThreads, kChT = (BN + TL::kThreads - 1) / TL::kThreads;
+  float row_scale[kRowsT], ch_scale[kChT], ch_bias[kChT];
+#pragma unroll
+  for (int i = 0; i < kRowsT; ++i) {
+    const int m = tid + i * TL::kThreads;
+    row_scale[i] = 0.0f;
+    if (m < BM && src_s[m] >= 0) row_scale[i] = as[src_s[m]];
+  }
+#pragma unroll
+  for (int i = 0; i < kChT; ++i) {
+    const int j = tid + i * TL::kThreads, u = j >> 4;   // SwiGLU: even tiles are gate, odd ones up
+    const int t = GLU ? ((u & 1) ? HT : 0) + min(u0 + (u >> 1), HT - 1) : min(u0 + u, NT - 1);
+    const int n = j < BN ? i8_channel(t, j & 15, N, glu) : -1;
+    ch_scale[i] = ch_bias[i] = 0.0f;
+    if (n >= 0) {
+      ch_scale[i] = wsc[(int64_t)e * N + n];
+      if (bias) ch_bias[i] = bias[(int64_t)e * N + n];
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  if (C >= NST)
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 1) * TL::kOpsW));
+  else
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  if (C > 0) read(0, ring);
+  int slot = 0;
+  for (int c = 0; c < C; ++c) {
+    const int next = slot == NST - 1 ? 0 : slot + 1;
+    read(1, ring + slot * TL::kStage);
+    multiply(0);
+    if (c + 1 < C) {
+      // this wavefront has read chunk c, and its copies of chunk c + 1 have landed (those of the
+      // chunks after it may be in flight); the barrier says so for every wavefront
+      if (c + NST <= C)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsW) & ~(15 << 8));
+      else
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0) & ~(15 << 8));
+      if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      if (c + NST < C) issue(slot);
+      read(0, ring + next * TL::kStage);
+    }
+    multiply(1);
+    slot = next;
+  }
+
+#pragma unroll
+  for (int i = 0; i < kRowsT; ++i)
+    if (tid + i * TL::kThreads < BM) scale_s[tid + i * TL::kThreads] = row_scale[i];
+#pragma unroll
+  for (int i = 0; i < kChT; ++i)
+    if (tid + i * TL::kThreads < BN) {
+      wsc_s[tid + i * TL::kThreads] = ch_scale[i];
+      bias_s[tid + i * TL::kThreads] = ch_bias[i];
+    }
+  lds_barrier();   // (and every group is done with its ring)
+
+  // 5. the groups' sums meet: a block's 16 sums of a lane lie as four quads of 256 x 4 bytes
+  i32x4_t* const red = reinterpret_cast<i32x4_t*>(lds);
+  if constexpr (TL::WK > 1) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          red[(((part * FN + f) * FM + m) * 4 + q) * kWave + lane] =
+              i32x4_t{acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]};
+    lds_barrier();
+  }
+  auto quad = [&](int f, int m, int q) {
+    if constexpr (TL::WK > 1) {
+      i32x4_t s = {0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < TL::WK; ++p) s += red[(((p * FN + f) * FM + m) * 4 + q) * kWave + lane];
+      return s;
+    } else {
+      return i32x4_t{acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]};
+    }
+  };
+
+  // 6. scales, bias, activation: a lane holds, for row m of the block, channels 8 q + 4 hi + i
+  // (q, i < 4) of each 32-channel block (SwiGLU: q = 0, 1 gate values, q + 2 the up values). The
+  // values go through LDS, where the rings were, and out as whole row pieces: stored from the
+  // lanes, 8 to 16 bytes of 32 rows at a time, they cost 15 % of a 512-token gate_up projection
+  constexpr int kSize = OUT == MOE_F32 ? 4 : 2;
+  constexpr int kCh = GLU ? BN / 2 : BN;                 // output channels of the workgroup
+  constexpr int kPitch = kCh * kSize + 16;
+  constexpr int kPassRows = TL::WK > 1 ? BM : TL::WM * 32;
+  static_assert(kPassRows * kPitch + TL::kRed <= TL::kRing, "LDS");
+  uint8_t* const stage = lds + TL::kRed;
+  auto emit = [&](int f, int m, int q, int lr) {         // lr: row of the pass
+    const float sa = scale_s[ml + m * 32];
+    const int j = (wn * FN + f) * 32 + 8 * q + 4 * hi;   // place in the workgroup's channels
+    const float4 sw = *reinterpret_cast<const float4*>(wsc_s + j);
+    const float4 sb = *reinterpret_cast<const float4*>(bias_s + j);
+    const i32x4_t t = quad(f, m, q);
+    float v[4] = {fmaf((float)t[0], sa * sw.x, sb.x), fmaf((float)t[1], sa * sw.y, sb.y),
+                  fmaf((float)t[2], sa * sw.z, sb.z), fmaf((float)t[3], sa * sw.w, sb.w)};
+    int ch = j;
+    if constexpr (GLU) {
+      const float4 uw = *reinterpret_cast<const float4*>(wsc_s + j + 16);
+      const float4 ub = *reinterpret_cast<const float4*>(bias_s + j + 16);
+      const i32x4_t u = quad(f, m, q + 2);
+      v[0] = i8_swiglu(v[0], fmaf((float)u[0], sa * uw.x, ub.x), alpha, limit);
+      v[1] = i8_swiglu(v[1], fmaf((float)u[1], sa * uw.y, ub.y), alpha, limit);
+      v[2] = i8_swiglu(v[2], fmaf((float)u[2], sa * uw.z, ub.z), alpha, limit);
+      v[3] = i8_swiglu(v[3], fmaf((float)u[3], sa * uw.w, ub.w), alpha, limit);
+      ch = (wn * FN + f) * 16 + 8 * q + 4 * hi;
+    }
+    uint8_t* const dst = stage + lr * kPitch + ch * kSize;
+    if constexpr (OUT == MOE_F32) {
+      *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[i] = OUT == MOE_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(v[i])) : f32_to_bf16_bits(v[i]);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+    }
+  };
+  // channel of place ch of the workgroup's output, or -1
+  auto channel = [&](int ch) {
+    if constexpr (GLU) {
+      const int n = u0 * 16 + ch;
+      return n < (N >> 1) ? n : -1;
+    }
+    const int t = u0 + (ch >> 4);
+    return t < NT ? i8_channel(t, ch & 15, N, glu) : -1;
+  };
+  auto store = [&](int m) {                               // the rows of pass m
+    auto row_of = [&](int lr) { return TL::WK > 1 ? lr : (lr >> 5) * FM * 32 + m * 32 + (lr & 31); };
+    if (vec) {
+      constexpr int kPer = 16 / kSize, kPieces = kCh / kPer;   // 16-byte pieces of a row
+      for (int i = tid; i < kPassRows * kPieces; i += TL::kThreads) {
+        const int lr = i / kPieces, ch = i % kPieces * kPer, mr = row_of(lr);
+        if (src_s[mr] < 0) continue;
+        const int n = channel(ch);
+        const uint8_t* from = stage + lr * kPitch + ch * kSize;
+        uint8_t* to = (uint8_t*)out + ((base + r0 + mr) * ld_out + n) * kSize;
+        if (n >= 0 && channel(ch + kPer - 1) >= 0) {
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+        } else {
+          for (int c = 0; c < kPer; ++c)
+            if (channel(ch + c) >= 0) {
+              if constexpr (kSize == 4)
+                ((uint32_t*)to)[c] = ((const uint32_t*)from)[c];
+              else
+                ((uint16_t*)to)[c] = ((const uint16_t*)from)[c];
+            }
+        }
+      }
+    } else {
+      for (int i = tid; i < kPassRows * kCh; i += TL::kThreads) {
+        const int lr = i / kCh, ch = i % kCh, mr = row_of(lr), n = channel(ch);
+        if (src_s[mr] < 0 || n < 0) continue;
+        const uint8_t* from = stage + lr * kPitch + ch * kSize;
+        uint8_t* to = (uint8_t*)out + ((base + r0 + mr) * ld_out + n) * kSize;
+        if constexpr (kSize == 4)
+          *(uint32_t*)to = *(const uint32_t*)from;
+        else
+          *(uint16_t*)to = *(const uint16_t*)from;
+      }
+    }
+  };
+  constexpr int QN = GLU ? 2 : 4;
+  if constexpr (TL::WK > 1) {   // the quads of the blocks are dealt to the wavefronts
+    for (int i = part; i < FM * FN * QN; i += TL::WK)
+      emit(i / (FM * QN), i / QN % FM, i % QN, i / QN % FM * 32 + l31);
+    lds_barrier();
+    store(0);
+  } else {
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      if (m) lds_barrier();   // the rows of the pass before are out
 #pragma unroll
       for (int f = 0; f < FN; ++f)
 #pragma unroll
-        for (int m = 0; m < FM; ++m)
-          acc[f][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[f], av[m], acc[f][m], 0, 0, 0);
-    }
-  }
-
-  // 5. scales, bias, activation: a lane holds, for row m of the block, channels 8 q + 4 hi + i
-  // (q, i < 4) of each 32-channel block (SwiGLU: q = 0, 1 gate values, q + 2 the up values)
-  const int F = N >> 1;
-#pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const int mr = ml + m * 32;
-    if (src_s[mr] < 0) continue;
-    const float sa = scale_s[mr];
-    const int64_t at = (base + r0 + mr) * ld_out;
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-#pragma unroll
-      for (int q = 0; q < (GLU ? 2 : 4); ++q) {
-        const int j = (wn * FN + f) * 32 + 8 * q + 4 * hi;   // place in the workgroup's channels
-        const float4 sw = *reinterpret_cast<const float4*>(wsc_s + j);
-        const float4 sb = *reinterpret_cast<const float4*>(bias_s + j);
-        float v[4] = {fmaf((float)acc[f][m][4 * q], sa * sw.x, sb.x),
-                      fmaf((float)acc[f][m][4 * q + 1], sa * sw.y, sb.y),
-                      fmaf((float)acc[f][m][4 * q + 2], sa * sw.z, sb.z),
-                      fmaf((float)acc[f][m][4 * q + 3], sa * sw.w, sb.w)};
-        int ch, some;   // first channel of the four, how many of them there are
-        if constexpr (GLU) {
-          const float4 uw = *reinterpret_cast<const float4*>(wsc_s + j + 16);
-          const float4 ub = *reinterpret_cast<const float4*>(bias_s + j + 16);
-          v[0] = i8_swiglu(v[0], fmaf((float)acc[f][m][8 + 4 * q], sa * uw.x, ub.x), alpha, limit);
-          v[1] = i8_swiglu(v[1], fmaf((float)acc[f][m][9 + 4 * q], sa * uw.y, ub.y), alpha, limit);
-          v[2] = i8_swiglu(v[2], fmaf((float)acc[f][m][10 + 4 * q], sa * uw.z, ub.z), alpha, limit);
-          v[3] = i8_swiglu(v[3], fmaf((float)acc[f][m][11 + 4 * q], sa * uw.w, ub.w), alpha, limit);
-          ch = (u0 + wn * FN + f) * 16 + 8 * q + 4 * hi;
-          some = F - ch;
-        } else {
-          const int tl = u0 + (wn * FN + f) * 2 + (q >> 1), half = glu && tl >= HT;
-          ch = (tl - half * HT) * 16 + 8 * (q & 1) + 4 * hi;
-          some = tl < NT ? (glu ? F : N) - ch : 0;
-          ch += half * F;
-        }
-        if (vec && some >= 4) {
-          if constexpr (OUT == MOE_F32) {
-            *reinterpret_cast<float4*>((float*)out + at + ch) = make_float4(v[0], v[1], v[2], v[3]);
-          } else {
-            uint32_t b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              b[i] = OUT == MOE_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(v[i]))
-                                    : f32_to_bf16_bits(v[i]);
-            *reinterpret_cast<uint2*>((uint16_t*)out + at + ch) =
-                make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < some) store_elem(out, at + ch + i, v[i], OUT);
-        }
-      }
+        for (int q = 0; q < QN; ++q) emit(f, m, q, wm * 32 + l31);
+      lds_barrier();
+      store(m);
     }
   }
 }
@@ -331,8 +456,8 @@ int launch_tile(const I8GemmArgs& g, hipStream_t st) {
   const int64_t grid = (mblocks * nblocks + 7) / 8 * 8;
   if (grid > 0x7FFFFFFFLL) return MOE_ESHAPE;
   constexpr int size = OUT == MOE_F32 ? 4 : 2;
-  const int vec = !((uintptr_t)g.out & (4 * size - 1)) && (g.ld_out & 3) == 0 &&
-                  (!w->glu || (w->N / 2) % 4 == 0);
+  const int vec = !((uintptr_t)g.out & 15) && g.ld_out * size % 16 == 0 &&
+                  (GLU || !w->glu || (w->N / 2) * size % 16 == 0);
   launch(i8_gemm_kernel<TL, GLU, ROUTED, OUT>, dim3((unsigned)grid), dim3(TL::kThreads), TL::kLds, st,
          g.a, g.as, g.a_row, g.a_rows, w->q, w->s, w->bias, w->E, w->N, w->K, w->glu, g.counts,
          g.basep, g.rows, g.mpad, (int)nblocks, g.alpha, g.limit, g.out, g.ld_out, vec);
@@ -372,5 +497,20 @@ int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, i
                               out, out_dt, ld_out, st);
   if (form == 1) return moe::launch_form<moe::I8Tile<64, 128, 1, 4, 6>>(g, glu, st);
   if (form == 2) return moe::launch_form<moe::I8Tile<128, 128, 2, 2, 4>>(g, glu, st);
+  if (form == 4) return moe::launch_form<moe::I8Tile<32, 32, 1, 1, 8, 4>>(g, glu, st);
+  if (form == 5) return moe::launch_form<moe::I8Tile<64, 32, 1, 1, 6, 4>>(g, glu, st);
+  if (form == 6) return moe::launch_form<moe::I8Tile<64, 64, 1, 1, 4, 4>>(g, glu, st);
+  if (form == 7) return moe::launch_form<moe::I8Tile<32, 64, 1, 1, 6, 4>>(g, glu, st);
+  if (form == 8) return moe::launch_form<moe::I8Tile<32, 128, 1, 4, 7>>(g, glu, st);
+  if (form == 9) return moe::launch_form<moe::I8Tile<64, 64, 1, 2, 6>>(g, glu, st);
+#define FORM(n, ...) if (form == n) return moe::launch_form<moe::I8Tile<__VA_ARGS__>>(g, glu, st);
+  FORM(10, 64, 256, 1, 8, 7)
+  FORM(11, 128, 256, 2, 4, 6)
+  FORM(12, 128, 256, 2, 2, 3)
+  FORM(13, 256, 128, 2, 2, 3)
+  FORM(14, 128, 128, 2, 2, 3)
+  FORM(15, 64, 128, 1, 4, 4)
+  FORM(19, 256, 256, 2, 2, 4)
+  FORM(20, 64, 128, 1, 4, 3)
   return moe::launch_form<moe::I8Tile<256, 256, 2, 4, 4>>(g, glu, st);
 }
