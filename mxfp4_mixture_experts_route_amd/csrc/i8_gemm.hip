@@ -1,6 +1,7 @@
-// 8-bit integer projections of many rows, dense or over the routed rows of every expert, with the
-// clamped SwiGLU as an optional epilogue; the function of i8_gemv.hip, bit for bit (the sums are
-// exact 32-bit integers).
+// 8-bit integer projections, dense or over the routed rows of every expert, with the clamped
+// SwiGLU as an optional epilogue: out = (sum_k aq wq) * (s_row * s_channel) + bias. The sums are
+// exact 32-bit integers (K <= 65536 keeps 128 * 128 * K below 2^31), so every tile and every split
+// of K gives the same bits.
 //
 // A workgroup computes BM rows of activations by BN channels. K goes in chunks of 64: the chunk's
 // weight tiles and activation rows are copied by LDS-DMA into a ring of NST buffers, NST - 1
@@ -28,12 +29,14 @@ struct I8Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, WK = WK_;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * WK * kWave;   // (waves of a group)
   static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;      // 32x32 blocks per wavefront
-  static constexpr int kOps = (BM + BN) / 16;                     // 1 KB copies per chunk
-  static constexpr int kOpsW = (kOps + kWaves - 1) / kWaves;      // of a wavefront
+  // 1 KB copies of a wavefront per chunk: weight tiles, then 16 activation rows each
+  static constexpr int kOpsB = BN / 16 / kWaves, kOpsA = (BM / 16 + kWaves - 1) / kWaves;
+  static constexpr int kOpsW = kOpsB + kOpsA;
   static constexpr int kStage = (BM + BN) * kI8Chunk;
   static constexpr int kRing = WK * NST * kStage;
   static constexpr int kRed = WK > 1 ? WK * BM * BN * 4 : 0;   // sums of the groups, where the rings were
   static constexpr int kLds = kRing + (BM + BN) * 8;   // + what the epilogue needs per row and channel
+  static_assert(BN / 16 % kWaves == 0, "every wavefront copies the same number of tiles");
   static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "whole blocks");
   static_assert(NST * kOpsW <= 63, "vmcnt range");
   static_assert(WK == 1 || kWaves == 1, "groups of one wavefront");
@@ -100,6 +103,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   // 1. the item: workgroups are dealt to the 8 XCDs round robin, so item numbers are dealt in 8
   // contiguous shares, and an XCD's L2 sees neighbouring items
   int e = 0, mb, nb;
+  bool once;   // the only block of rows that reads these weights
   {
     const int x = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3;
     if constexpr (ROUTED) {
@@ -114,9 +118,11 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
       const int in = item - (blk0 - m0) * nblocks;
       nb = in / eb;
       mb = in - nb * eb;
+      once = eb == 1;
     } else {
       const int mblocks = (int)((rows + BM - 1) / BM);
       const int total = mblocks * nblocks, per = (total + 7) >> 3;
+      once = mblocks == 1;
       const int item = x * per + i;
       if (i >= per || item >= total) return;
       // groups of 8 row blocks, channels ascending inside a group: a share is a near-square
@@ -159,36 +165,46 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   const int KP = i8_pitch(K), CK = KP / kI8Chunk;
   const int cb = CK * part / TL::WK, C = CK * (part + 1) / TL::WK - cb;   // this group's chunks
   uint8_t* const ring = lds + part * NST * TL::kStage;
-  // operation number i of this wavefront; a surplus one repeats the last (the same bytes to the
-  // same place)
-  auto op = [&](int i) { return min(wave + i * TL::kWaves, TL::kOps - 1); };
+  // tile or group of 16 rows that copy i of this wavefront takes; a surplus group repeats the last
+  // one (the same bytes to the same place)
+  auto tile_of = [&](int i) { return wave + i * TL::kWaves; };
+  auto rows_of = [&](int i) { return min(wave + i * TL::kWaves, BM / 16 - 1); };
   // each operation: a 64-bit scalar address that steps through the chunks and a 32-bit offset per
   // lane (the rows of a routed product lie within 4 GB, a dense one starts at its own rows)
   const int64_t wstep = (int64_t)NT * kI8TileBytes;
   const int8_t* wbase = wq + ((int64_t)e * CK + cb) * wstep;
   const int8_t* abase = a + (ROUTED ? 0 : r0 * KP) + cb * kI8Chunk;
   const int first = ROUTED ? 0 : (int)r0;
-  uint32_t voff[TL::kOpsW];
+  uint32_t wvoff[TL::kOpsB], avoff[TL::kOpsA];
 #pragma unroll
-  for (int i = 0; i < TL::kOpsW; ++i) {
-    const int j = op(i);
-    if (j < BN / 16) {
-      // tiles past the last one repeat it; their channels are not stored
-      const int t = GLU ? (j & 1) * HT + min(u0 + (j >> 1), HT - 1) : min(u0 + j, NT - 1);
-      voff[i] = (uint32_t)t * kI8TileBytes + lane * 16;
-    } else {
-      const int m = (j - BN / 16) * 16 + (lane >> 2);
-      const int piece = (lane & 3) ^ ((m >> 2) & 3);
-      voff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
-    }
+  for (int i = 0; i < TL::kOpsB; ++i) {
+    // tiles past the last one repeat it; their channels are not stored
+    const int j = tile_of(i);
+    const int t = GLU ? (j & 1) * HT + min(u0 + (j >> 1), HT - 1) : min(u0 + j, NT - 1);
+    wvoff[i] = (uint32_t)t * kI8TileBytes + lane * 16;
   }
-  auto issue = [&](int slot) {
 #pragma unroll
-    for (int i = 0; i < TL::kOpsW; ++i) {
-      const int j = op(i);
-      __builtin_amdgcn_global_load_lds((gptr_t)((j < BN / 16 ? wbase : abase) + voff[i]),
-                                       (lptr_t)(ring + slot * TL::kStage + j * 1024), 16, 0, 0);
+  for (int i = 0; i < TL::kOpsA; ++i) {
+    const int m = rows_of(i) * 16 + (lane >> 2);
+    const int piece = (lane & 3) ^ ((m >> 2) & 3);
+    avoff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
+  }
+  // Weights that no other workgroup reads carry the nontemporal hint, so that they do not push
+  // the activations out of L2 (64 tokens: 92 -> 81 us); with more row blocks an expert the others
+  // find them there (512 tokens with the hint: 122 -> 138 us)
+  auto issue = [&](int slot) {
+    uint8_t* const st = ring + slot * TL::kStage;
+#pragma unroll
+    for (int i = 0; i < TL::kOpsB; ++i) {
+      if (once)
+        __builtin_amdgcn_global_load_lds((gptr_t)(wbase + wvoff[i]), (lptr_t)(st + tile_of(i) * 1024), 16, 0, 2);
+      else
+        __builtin_amdgcn_global_load_lds((gptr_t)(wbase + wvoff[i]), (lptr_t)(st + tile_of(i) * 1024), 16, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < TL::kOpsA; ++i)
+      __builtin_amdgcn_global_load_lds((gptr_t)(abase + avoff[i]),
+                                       (lptr_t)(st + BN * kI8Chunk + rows_of(i) * 1024), 16, 0, 0);
     wbase += wstep;
     abase += kI8Chunk;
   };
@@ -234,7 +250,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     if (s < C) issue(s);
   __builtin_amdgcn_sched_barrier(0);
   // what the epilogue needs goes out behind the first copies: the scale of a row, scale and bias
-  // of a channel, up to kExtra values a thread
+  // of a channel
   constexpr int kRowsT = (BM + TL::kThreads - 1) / TL::kThreads, kChT = (BN + TL::kThreads - 1) / TL::kThreads;
   float row_scale[kRowsT], ch_scale[kChT], ch_bias[kChT];
 #pragma unroll
@@ -464,53 +480,68 @@ int launch_tile(const I8GemmArgs& g, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }
 
+// The tiles. LDS holds three workgroups of I8Mid or I8Wide a CU, one of the others.
+using I8Few = I8Tile<32, 32, 1, 1, 8, 4>;     // few rows: K split over four wavefronts
+using I8Low = I8Tile<32, 64, 1, 1, 6, 4>;
+using I8Half = I8Tile<64, 64, 1, 1, 4, 4>;
+using I8Mid = I8Tile<64, 128, 1, 4, 3>;
+using I8Wide = I8Tile<128, 128, 2, 2, 3>;
+using I8Big = I8Tile<256, 256, 2, 4, 4>;
+
 template <class TL>
-int launch_form(const I8GemmArgs& g, bool glu, hipStream_t st) {
-  if (g.counts)
-    return glu ? launch_tile<TL, true, true, MOE_BF16>(g, st)
-               : launch_tile<TL, false, true, MOE_F32>(g, st);
+int launch_dense(const I8GemmArgs& g, hipStream_t st) {
   return g.out_dt == MOE_F32   ? launch_tile<TL, false, false, MOE_F32>(g, st)
          : g.out_dt == MOE_F16 ? launch_tile<TL, false, false, MOE_F16>(g, st)
                                : launch_tile<TL, false, false, MOE_BF16>(g, st);
 }
 
-}  // namespace moe
+template <class TL>
+int launch_routed(const I8GemmArgs& g, bool glu, hipStream_t st) {
+  return glu ? launch_tile<TL, true, true, MOE_BF16>(g, st)
+             : launch_tile<TL, false, true, MOE_F32>(g, st);
+}
 
-int moe_launch_i8_gemv(const int8_t* a, const float* as, const int32_t* a_row, int64_t a_rows,
-                       const i8_experts* w, const int32_t* counts, const int32_t* basep,
-                       int64_t rows, int64_t mpad, int act, float alpha, float limit, void* out,
-                       int out_dt, int64_t ld_out, hipStream_t st);
+// Time of a dense product per chunk of K, in ns: a CU goes through ceil(tiles / 256) tiles, `one`
+// ns a chunk where that is one and `each` ns for each of several, as measured at 2880 -> 5760
+// channels and (I8Big) 8192 -> 8192 on 256 CUs. The least of them names the tile: at 64 rows
+// I8Low takes 8.0 us, I8Few 11, I8Half 10, I8Mid 14; at 128 rows I8Half 10.6, I8Low 13.9, I8Mid
+// 15; at 512 rows I8Mid 20, I8Wide 21.5, I8Half 28; at 2048 rows I8Wide 46, I8Big 50, I8Mid 52;
+// 4096 rows of 8192: I8Big 266, I8Wide 306.
+template <class TL>
+double chunk_ns(int64_t rows, int units, double one, double each) {
+  const int64_t tiles = (rows + TL::BM - 1) / TL::BM * ((units + TL::BN / 16 - 1) / (TL::BN / 16));
+  const int64_t rounds = (tiles + 255) / 256;
+  return rounds == 1 ? one : (double)rounds * each;
+}
+
+}  // namespace moe
 
 int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, int64_t a_rows,
                        const i8_experts* w, const int32_t* counts, const int32_t* basep,
                        int64_t rows, int64_t mpad, int act, float alpha, float limit, void* out,
                        int out_dt, int64_t ld_out, hipStream_t st) {
-  const bool glu = act == MOE_ACT_SWIGLU_OAI;
-  const moe::I8GemmArgs g{a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
-                          out, out_dt, ld_out};
-  // rows per product (routed: the mean over the experts, padding included)
-  const int64_t per = counts ? mpad / w->E : rows;
-  int form = per <= 24 ? 0 : per <= 96 ? 1 : 2;
-  if (form == 2 && ((rows + 255) / 256) * ((w->N + 255) / 256) >= 256) form = 3;
-  if (form == 0)
-    return moe_launch_i8_gemv(a, as, a_row, a_rows, w, counts, basep, rows, mpad, act, alpha, limit,
-                              out, out_dt, ld_out, st);
-  if (form == 1) return moe::launch_form<moe::I8Tile<64, 128, 1, 4, 6>>(g, glu, st);
-  if (form == 2) return moe::launch_form<moe::I8Tile<128, 128, 2, 2, 4>>(g, glu, st);
-  if (form == 4) return moe::launch_form<moe::I8Tile<32, 32, 1, 1, 8, 4>>(g, glu, st);
-  if (form == 5) return moe::launch_form<moe::I8Tile<64, 32, 1, 1, 6, 4>>(g, glu, st);
-  if (form == 6) return moe::launch_form<moe::I8Tile<64, 64, 1, 1, 4, 4>>(g, glu, st);
-  if (form == 7) return moe::launch_form<moe::I8Tile<32, 64, 1, 1, 6, 4>>(g, glu, st);
-  if (form == 8) return moe::launch_form<moe::I8Tile<32, 128, 1, 4, 7>>(g, glu, st);
-  if (form == 9) return moe::launch_form<moe::I8Tile<64, 64, 1, 2, 6>>(g, glu, st);
-#define FORM(n, ...) if (form == n) return moe::launch_form<moe::I8Tile<__VA_ARGS__>>(g, glu, st);
-  FORM(10, 64, 256, 1, 8, 7)
-  FORM(11, 128, 256, 2, 4, 6)
-  FORM(12, 128, 256, 2, 2, 3)
-  FORM(13, 256, 128, 2, 2, 3)
-  FORM(14, 128, 128, 2, 2, 3)
-  FORM(15, 64, 128, 1, 4, 4)
-  FORM(19, 256, 256, 2, 2, 4)
-  FORM(20, 64, 128, 1, 4, 3)
-  return moe::launch_form<moe::I8Tile<256, 256, 2, 4, 4>>(g, glu, st);
+  using namespace moe;
+  const I8GemmArgs g{a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
+                     out, out_dt, ld_out};
+  if (counts) {
+    // rows of an expert, padding included: below 64 most experts have one block of I8Mid (256
+    // tokens, 32 rows an expert: gate_up 94 us, I8Wide 99; 512 tokens: 123 and 114 us)
+    const bool glu = act == MOE_ACT_SWIGLU_OAI;
+    return mpad / w->E < 64 ? launch_routed<I8Mid>(g, glu, st) : launch_routed<I8Wide>(g, glu, st);
+  }
+  const int units = i8_tiles(w->N, w->glu);
+  const double ns[] = {chunk_ns<I8Few>(rows, units, 45, 70),   chunk_ns<I8Low>(rows, units, 78, 100),
+                       chunk_ns<I8Half>(rows, units, 140, 155), chunk_ns<I8Mid>(rows, units, 245, 168),
+                       chunk_ns<I8Wide>(rows, units, 360, 300), chunk_ns<I8Big>(rows, units, 1040, 1040)};
+  int best = 0;
+  for (int i = 1; i < 6; ++i)
+    if (ns[i] < ns[best]) best = i;
+  switch (best) {
+    case 0: return launch_dense<I8Few>(g, st);
+    case 1: return launch_dense<I8Low>(g, st);
+    case 2: return launch_dense<I8Half>(g, st);
+    case 3: return launch_dense<I8Mid>(g, st);
+    case 4: return launch_dense<I8Wide>(g, st);
+    default: return launch_dense<I8Big>(g, st);
+  }
 }
