@@ -41,6 +41,21 @@ __device__ __forceinline__ int i8_channel(int t, int r, int N, int glu) {
   return n < F ? half * F + n : -1;
 }
 
+// float -> bf16 bits by the hardware conversion (round to nearest even, subnormals kept; checked
+// against the integer rounding of f32_to_bf16_bits over every exponent), a pair at a time or one.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const bf16x2_t p = {(__bf16)lo, (__bf16)hi};
+  uint32_t u;
+  __builtin_memcpy(&u, &p, sizeof(u));
+  return u;
+}
+__device__ __forceinline__ uint16_t bf16_one(float v) {
+  const __bf16 b = (__bf16)v;
+  uint16_t u;
+  __builtin_memcpy(&u, &b, sizeof(u));
+  return u;
+}
+
 // Typed element access (MOE_BF16 / MOE_F16 / MOE_F32).
 template <int DT>
 __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
@@ -54,7 +69,7 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v, int dt) 
   else if (dt == MOE_F16)
     ((__half*)p)[i] = __float2half_rn(v);
   else
-    ((uint16_t*)p)[i] = (uint16_t)f32_to_bf16_bits(v);
+    ((uint16_t*)p)[i] = bf16_one(v);
 }
 
 // Row quantization: with m the row's largest magnitude, the scale is m / 127 (rounded to f32) and

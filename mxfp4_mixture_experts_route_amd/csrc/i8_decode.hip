@@ -162,7 +162,7 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   if (tid < kI8TileRows && n < F) {
     const float gate = fmaf((float)(red[0][tid] + red[1][tid]), z.s * sg, bg);
     const float up = fmaf((float)(red[2][tid] + red[3][tid]), z.s * su, bu);
-    h[(int64_t)j * F + n] = (uint16_t)f32_to_bf16_bits(i8_swiglu(gate, up, alpha, limit));
+    h[(int64_t)j * F + n] = bf16_one(i8_swiglu(gate, up, alpha, limit));
   }
 }
 
@@ -366,7 +366,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
       const float sa = sx[m];
       const float gate = fmaf((float)(rd[0][from][i] + rd[1][from][i]), sa * sg, bg);
       const float up = fmaf((float)(rd[2][from][i] + rd[3][from][i]), sa * su, bu);
-      h[(int64_t)list[m] * F + n] = (uint16_t)f32_to_bf16_bits(i8_swiglu(gate, up, alpha, limit));
+      h[(int64_t)list[m] * F + n] = bf16_one(i8_swiglu(gate, up, alpha, limit));
     }
   }
 }

@@ -144,23 +144,23 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   const int live = (int)min((int64_t)BM, count - r0);
   if (live <= 0) return;
 
-  // 2. source row of every row of the block
+  // 2. the source rows of the block are on their way while the first weights go out
   const int NT = i8_tiles(N, glu), HT = i8_half_tiles(N, glu);
   const int u0 = nb * kUnits;
   int* const src_s = reinterpret_cast<int*>(lds + TL::kRing);
   float* const scale_s = reinterpret_cast<float*>(src_s + BM);
   float* const wsc_s = scale_s + BM;
   float* const bias_s = wsc_s + BN;
-  for (int m = tid; m < BM; m += TL::kThreads) {
+  constexpr int kRowsT = (BM + TL::kThreads - 1) / TL::kThreads;
+  int src_r[kRowsT];
+#pragma unroll
+  for (int i = 0; i < kRowsT; ++i) {
+    const int m = tid + i * TL::kThreads;
     int64_t src = -1;
-    if (m < live) {
-      src = ROUTED && a_row ? (int64_t)a_row[base + r0 + m] : base + r0 + m;
-      if ((uint64_t)src >= (uint64_t)a_rows) src = -1;   // such a row is not stored
-    }
-    src_s[m] = (int)src;
+    if (m < live) src = ROUTED && a_row ? (int64_t)a_row[base + r0 + m] : base + r0 + m;
+    src_r[i] = (int)src;
   }
-  __syncthreads();
-
+  __builtin_amdgcn_sched_barrier(0);
   // 3. copies of a chunk: operation j < BN / 16 is weight tile j, the others 16 rows each
   const int KP = i8_pitch(K), CK = KP / kI8Chunk;
   const int cb = CK * part / TL::WK, C = CK * (part + 1) / TL::WK - cb;   // this group's chunks
@@ -183,16 +183,10 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     const int t = GLU ? (j & 1) * HT + min(u0 + (j >> 1), HT - 1) : min(u0 + j, NT - 1);
     wvoff[i] = (uint32_t)t * kI8TileBytes + lane * 16;
   }
-#pragma unroll
-  for (int i = 0; i < TL::kOpsA; ++i) {
-    const int m = rows_of(i) * 16 + (lane >> 2);
-    const int piece = (lane & 3) ^ ((m >> 2) & 3);
-    avoff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
-  }
   // Weights that no other workgroup reads carry the nontemporal hint, so that they do not push
   // the activations out of L2 (64 tokens: 92 -> 81 us); with more row blocks an expert the others
   // find them there (512 tokens with the hint: 122 -> 138 us)
-  auto issue = [&](int slot) {
+  auto issue_w = [&](int slot) {
     uint8_t* const st = ring + slot * TL::kStage;
 #pragma unroll
     for (int i = 0; i < TL::kOpsB; ++i) {
@@ -201,13 +195,37 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
       else
         __builtin_amdgcn_global_load_lds((gptr_t)(wbase + wvoff[i]), (lptr_t)(st + tile_of(i) * 1024), 16, 0, 0);
     }
+    wbase += wstep;
+  };
+  auto issue_a = [&](int slot) {
+    uint8_t* const st = ring + slot * TL::kStage;
 #pragma unroll
     for (int i = 0; i < TL::kOpsA; ++i)
       __builtin_amdgcn_global_load_lds((gptr_t)(abase + avoff[i]),
                                        (lptr_t)(st + BN * kI8Chunk + rows_of(i) * 1024), 16, 0, 0);
-    wbase += wstep;
     abase += kI8Chunk;
   };
+#pragma unroll
+  for (int s = 0; s < NST; ++s)
+    if (s < C) issue_w(s);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < kRowsT; ++i) {
+    const int m = tid + i * TL::kThreads;
+    // a source row out of range: the row is not stored
+    if (m < BM) src_s[m] = (uint64_t)(int64_t)src_r[i] < (uint64_t)a_rows ? src_r[i] : -1;
+  }
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < TL::kOpsA; ++i) {
+    const int m = rows_of(i) * 16 + (lane >> 2);
+    const int piece = (lane & 3) ^ ((m >> 2) & 3);
+    avoff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
+  }
+#pragma unroll
+  for (int s = 0; s < NST; ++s)
+    if (s < C) issue_a(s);
+  __builtin_amdgcn_sched_barrier(0);
 
   // 4. the K loop
   const int wm = wave % TL::WM, wn = wave / TL::WM;
@@ -245,13 +263,9 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
         acc[f][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[h][f], av[h][m], acc[f][m], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-#pragma unroll
-  for (int s = 0; s < NST; ++s)
-    if (s < C) issue(s);
-  __builtin_amdgcn_sched_barrier(0);
   // what the epilogue needs goes out behind the first copies: the scale of a row, scale and bias
   // of a channel
-  constexpr int kRowsT = (BM + TL::kThreads - 1) / TL::kThreads, kChT = (BN + TL::kThreads - 1) / TL::kThreads;
+  constexpr int kChT = (BN + TL::kThreads - 1) / TL::kThreads;
   float row_scale[kRowsT], ch_scale[kChT], ch_bias[kChT];
 #pragma unroll
   for (int i = 0; i < kRowsT; ++i) {
@@ -271,8 +285,9 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     }
   }
   __builtin_amdgcn_sched_barrier(0);
+  // (the activations' copies of the first chunks lie behind all their weights')
   if (C >= NST)
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 1) * TL::kOpsW));
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 1) * TL::kOpsA));
   else
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
@@ -286,13 +301,18 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     if (c + 1 < C) {
       // this wavefront has read chunk c, and its copies of chunk c + 1 have landed (those of the
       // chunks after it may be in flight); the barrier says so for every wavefront
-      if (c + NST <= C)
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsW) & ~(15 << 8));
-      else
+      if (c + NST > C)
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0) & ~(15 << 8));
+      else if (c < NST - 1)   // in flight behind it: the activations' copies of NST - 2 - c chunks at least
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsA) & ~(15 << 8));
+      else
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsW) & ~(15 << 8));
       if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      if (c + NST < C) issue(slot);
+      if (c + NST < C) {
+        issue_w(slot);
+        issue_a(slot);
+      }
       read(0, ring + next * TL::kStage);
     }
     multiply(1);
@@ -341,7 +361,10 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   constexpr int kSize = OUT == MOE_F32 ? 4 : 2;
   constexpr int kCh = GLU ? BN / 2 : BN;                 // output channels of the workgroup
   constexpr int kPitch = kCh * kSize + 16;
-  constexpr int kPassRows = TL::WK > 1 ? BM : TL::WM * 32;
+  // all rows at once where they fit, else one 32-row block of every wavefront after the other
+  constexpr bool kAll = BM * kPitch + TL::kRed <= TL::kRing;
+  static_assert(TL::WK == 1 || kAll, "LDS");
+  constexpr int kPassRows = kAll ? BM : TL::WM * 32;
   static_assert(kPassRows * kPitch + TL::kRed <= TL::kRing, "LDS");
   uint8_t* const stage = lds + TL::kRed;
   auto emit = [&](int f, int m, int q, int lr) {         // lr: row of the pass
@@ -367,11 +390,14 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     if constexpr (OUT == MOE_F32) {
       *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-      uint32_t b[4];
+      if constexpr (OUT == MOE_F16) {
+        uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[i] = OUT == MOE_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(v[i])) : f32_to_bf16_bits(v[i]);
-      *reinterpret_cast<uint2*>(dst) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        for (int i = 0; i < 4; ++i) b[i] = (uint32_t)__half_as_ushort(__float2half_rn(v[i]));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+      } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+      }
     }
   };
   // channel of place ch of the workgroup's output, or -1
@@ -384,7 +410,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     return t < NT ? i8_channel(t, ch & 15, N, glu) : -1;
   };
   auto store = [&](int m) {                               // the rows of pass m
-    auto row_of = [&](int lr) { return TL::WK > 1 ? lr : (lr >> 5) * FM * 32 + m * 32 + (lr & 31); };
+    auto row_of = [&](int lr) { return kAll ? lr : (lr >> 5) * FM * 32 + m * 32 + (lr & 31); };
     if (vec) {
       constexpr int kPer = 16 / kSize, kPieces = kCh / kPer;   // 16-byte pieces of a row
       for (int i = tid; i < kPassRows * kPieces; i += TL::kThreads) {
@@ -427,13 +453,16 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   } else {
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
-      if (m) lds_barrier();   // the rows of the pass before are out
+      if (!kAll && m) lds_barrier();   // the rows of the pass before are out
+      if ((wm * FM + m) * 32 < live)   // (blocks of 32 rows past the last are not formed)
 #pragma unroll
       for (int f = 0; f < FN; ++f)
 #pragma unroll
-        for (int q = 0; q < QN; ++q) emit(f, m, q, wm * 32 + l31);
-      lds_barrier();
-      store(m);
+        for (int q = 0; q < QN; ++q) emit(f, m, q, kAll ? ml + m * 32 : wm * 32 + l31);
+      if (!kAll || m == FM - 1) {
+        lds_barrier();
+        store(m);
+      }
     }
   }
 }

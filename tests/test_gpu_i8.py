@@ -552,3 +552,24 @@ def test_refusals_before_any_launch():
         moe.i8_gemm(aq[:, :32].contiguous(), as_, W)
     with pytest.raises(ValueError):
         moe.i8_moe_decode(torch.randn(3, 4, device="cuda"), x, W, W, 1)
+
+
+@pytest.mark.parametrize("rows", [2, 40])
+def test_outputs_are_rounded_over_the_whole_range(rows):
+    """A one-channel-per-value projection whose outputs cover every bf16 exponent, subnormals, ties
+    and both signs among them: the stored value is torch's rounding of the fp32 one."""
+    N, K = 2048, 64
+    q = torch.zeros(1, N, K, dtype=torch.int8, device="cuda")
+    q[0, :, 0] = 1
+    g = rng(3)
+    s = torch.exp2(torch.randint(-140, 120, (1, N), generator=g, device="cuda").double()) * \
+        (1 + torch.randint(0, 512, (1, N), generator=g, device="cuda").double() / 512)
+    W = moe.I8Experts(q, s.float())
+    x = torch.zeros(rows, K, device="cuda")
+    x[:, 0] = 127.0                                     # code 127, scale 1
+    x[1] = -x[1]
+    full = moe.i8_linear(x, W, out_dtype=F32)
+    assert torch.equal(full[0], (s[0] * 127.0).float())
+    assert torch.equal(moe.i8_linear(x, W, out_dtype=BF16), full.to(BF16))
+    half = moe.i8_linear(x, W, out_dtype=F16)
+    assert torch.equal(half, full.to(F16))
