@@ -418,7 +418,7 @@ int mx4_moe_decode_persistent_static(const float* logits, const uint16_t* x, int
  * keep 8-bit activations to the CPU; this format on the GPU is outside them.
  *
  * Quantized rows: row r of K values has its codes (int8, in [-127, 127]) at q + r*KP, KP =
- * roundup(K, 64), the KP - K padding codes 0, and its scale at s[r]; value i stands for
+ * roundup(K, 128), the KP - K padding codes 0, and its scale at s[r]; value i stands for
  * q[i] * s[r].
  */
 typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
@@ -433,7 +433,7 @@ typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
  *
  * Tiled layout: an expert's matrix is cut into tiles of 16 rows by 64 columns (1 KB), zeros past
  * N (past F in each half when glu) and K. With NT = roundup(N, 16)/16 (glu: 2 * roundup(F, 16)/16)
- * tiles of rows and C = KP/64 chunks of columns, tile (c, t) of expert e starts at byte
+ * tiles of rows and C = roundup(K, 64)/64 chunks of columns, tile (c, t) of expert e starts at byte
  * 1024 * ((e*C + c)*NT + t); its byte 256*p + 16*r + i is column 64c + 16p + i of row r, which is
  * the lane order of the MFMA operand, so a wavefront reads a tile as one contiguous run.
  */
@@ -518,7 +518,7 @@ int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t
  * rho = t*k + s. An expert is read once however many of the tokens picked it.
  *   logits f32 [T][E];  x bf16 [T][D];  w_gu: glu = 1, N = 2F, K = D;  w_dn: glu = 0, N = D, K = F
  *   ids i32 [T][k], w f32 [T][k] out (as moe_route_topk);  h bf16 [T*k][F] out
- *   q_ws int8 [T*k][roundup(F, 64)], s_ws f32 [T*k]: scratch that the call may write and leaves
+ *   q_ws int8 [T*k][roundup(F, 128)], s_ws f32 [T*k]: scratch that the call may write and leaves
  *   without meaning; both may be NULL for T*k <= 16 and F <= 4096. Calls that can run concurrently
  *   need distinct scratch.
  *   d f32 [T*k][D] out or NULL (then never written);  y y_dtype [T][D] out

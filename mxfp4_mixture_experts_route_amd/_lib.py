@@ -545,8 +545,8 @@ def _i8_weights(w, name: str, dev: int) -> None:
 
 
 def i8_pitch(K: int) -> int:
-    """Row pitch in bytes of quantized rows of K values: K padded to a multiple of 64."""
-    return (K + 63) // 64 * 64
+    """Row pitch in bytes of quantized rows of K values: K padded to a multiple of 128."""
+    return (K + 127) // 128 * 128
 
 
 def i8_row_buffers(rows: int, K: int, device="cuda"):

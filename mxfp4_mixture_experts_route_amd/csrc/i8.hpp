@@ -15,10 +15,13 @@ constexpr int kI8Chunk = 64;        // K values of a weight tile (one 16x16x64 M
 constexpr int kI8TileRows = 16;     // weight rows of a tile
 constexpr int kI8TileBytes = kI8Chunk * kI8TileRows;
 
-// Row pitch of quantized rows: K padded (with zeros) to whole chunks.
-__host__ __device__ __forceinline__ int i8_pitch(int K) {
-  return (K + kI8Chunk - 1) & ~(kI8Chunk - 1);
-}
+// Row pitch of quantized rows: K padded (with zeros) to whole cache lines of 128 bytes. A row is
+// read in pieces: of 64 bytes they would take twice as long (every load moves whole lines: reads
+// of 64-byte pieces reach 17 TB/s from L2 and 3.6 from memory, of 128 bytes 36 and 7).
+__host__ __device__ __forceinline__ int i8_pitch(int K) { return (K + 127) & ~127; }
+
+// Chunks of 64 K values of the packed weights.
+__host__ __device__ __forceinline__ int i8_chunks(int K) { return (K + kI8Chunk - 1) / kI8Chunk; }
 
 // Weight tiles of an expert: N rows in tiles of 16, or, packed for SwiGLU, each half (gate rows,
 // up rows) in tiles of its own, so that a gate tile and its up tile always match row for row.

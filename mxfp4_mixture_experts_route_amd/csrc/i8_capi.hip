@@ -21,7 +21,7 @@ int check_stack(const i8_experts* w) {
   if (w->glu != 0 && w->glu != 1) return MOE_EINVAL;
   if (w->E > MOE_MAX_E || w->K > MOE_I8_MAX_K || (w->glu && (w->N & 1))) return MOE_ESHAPE;
   // one expert's packed weights are addressed with 31 bits
-  if ((int64_t)moe::i8_tiles(w->N, w->glu) * 16 * moe::i8_pitch(w->K) >= (int64_t)1 << 31)
+  if ((int64_t)moe::i8_tiles(w->N, w->glu) * moe::i8_chunks(w->K) * moe::kI8TileBytes >= (int64_t)1 << 31)
     return MOE_ESHAPE;
   return MOE_OK;
 }

@@ -127,7 +127,7 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   const int e = __builtin_amdgcn_readfirstlane(route_one(logits, lv, E, k, j, keys[wave]));
   if (E > kWave) row.load(x, K);       // (the routing of more experts needs the registers)
 
-  const int C = i8_pitch(K) / kI8Chunk, NT = i8_tiles(N, 1), HT = i8_half_tiles(N, 1);
+  const int C = i8_chunks(K), NT = i8_tiles(N, 1), HT = i8_half_tiles(N, 1);
   const int part = wave & 1, tile = (wave >> 1) ? HT + unit : unit;
   const int cb = C * part / 2, len = C * (part + 1) / 2 - cb;
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
@@ -186,7 +186,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
   row.load(h + (int64_t)slot * F, F);
   __builtin_amdgcn_sched_barrier(0);
   e = __builtin_amdgcn_readfirstlane(min(max(e, 0), E - 1));
-  const int C = i8_pitch(F) / kI8Chunk, NT = i8_tiles(D, 0);
+  const int C = i8_chunks(F), NT = i8_tiles(D, 0);
   const int cb = C * part / parts, len = C * (part + 1) / parts - cb;
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step);
@@ -261,7 +261,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   const int item = (int)blockIdx.x - 1;
   const int groups = (units + upw - 1) / upw, j = item / groups;
   const int ubase = (item - j * groups) * upw, uend = min(ubase + upw, units);
-  const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), C = KP / kI8Chunk;
+  const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), C = i8_chunks(K);
 
   // 1. routing
   if (tid < MOE_MAX_E / 32) bits[tid] = 0u;
@@ -437,7 +437,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int R = T * k, unit = (int)blockIdx.x;
-  const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = FP / kI8Chunk, NT = i8_tiles(D, 0);
+  const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = i8_chunks(F), NT = i8_tiles(D, 0);
 
   for (int i = tid; i < R * kI8TileRows; i += kI8DownThreads) (&acc_s[0][0])[i] = 0;
   if (ROWS && tid < R) sh[tid] = hs[tid];
@@ -582,8 +582,8 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
   const int R = (int)T * k, units = moe::i8_half_tiles(N, 1);
   const int64_t xrow = moe::i8_lds_pitch(moe::i8_pitch(D)), hrow = moe::i8_lds_pitch(moe::i8_pitch(F));
   if (T * xrow > (int64_t)moe::kI8DecMaxLds ||
-      (int64_t)units * 32 * moe::i8_pitch(D) >= (int64_t)1 << 31 ||
-      (int64_t)moe::i8_tiles(D, 0) * 16 * moe::i8_pitch(F) >= (int64_t)1 << 31)
+      (int64_t)units * 2 * moe::i8_chunks(D) * moe::kI8TileBytes >= (int64_t)1 << 31 ||
+      (int64_t)moe::i8_tiles(D, 0) * moe::i8_chunks(F) * moe::kI8TileBytes >= (int64_t)1 << 31)
     return MOE_ESHAPE;
   const bool own_rows = R <= moe::kI8LdsRows && R * hrow <= (int64_t)moe::kI8DecMaxLds;
   if (!own_rows) {
@@ -607,7 +607,7 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
   const int fast1 = D % 8 == 0 && D <= moe::kI8DecVec * 8 * moe::kWave;
   const int fast2 = F % 8 == 0 && F <= moe::kI8DecVec * 8 * moe::kWave;
   if (T == 1 && fast1 && fast2) {
-    const int Cd = moe::i8_pitch(D) / moe::kI8Chunk, Cf = moe::i8_pitch(F) / moe::kI8Chunk;
+    const int Cd = moe::i8_chunks(D), Cf = moe::i8_chunks(F);
     // launch 2: 16 wavefronts, or as many as there are slots and chunks for
     int parts = 16 / k;
     while (parts > 1 && Cf < 4 * parts) --parts;

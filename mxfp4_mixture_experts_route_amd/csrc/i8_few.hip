@@ -29,7 +29,7 @@ i8_few_kernel(const void* __restrict__ x, int64_t ld, int rows, const int8_t* __
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int unit = (int)blockIdx.x, NT = i8_tiles(N, glu);
-  const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), C = KP / kI8Chunk;
+  const int KP = i8_pitch(K), LP = i8_lds_pitch(KP), C = i8_chunks(K);
   const int cb = C * wave / kWaves, len = C * (wave + 1) / kWaves - cb;
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq, (uint32_t)C * step);

@@ -3,14 +3,18 @@
 // exact 32-bit integers (K <= 65536 keeps 128 * 128 * K below 2^31), so every tile and every split
 // of K gives the same bits.
 //
-// A workgroup computes BM rows of activations by BN channels. K goes in chunks of 64: the chunk's
-// weight tiles and activation rows are copied by LDS-DMA into a ring of NST buffers, NST - 1
-// chunks ahead, so that one barrier per chunk is all the synchronization there is, and the
-// products run on v_mfma_i32_32x32x32_i8 (weights = A, activations = B).
+// A workgroup computes BM rows of activations by BN channels on v_mfma_i32_32x32x32_i8 (weights =
+// A, activations = B). K goes in steps of 128, a whole cache line of an activation row (see
+// i8_pitch), that is two chunks of the packed weights. Two forms:
+//  * I8Tile: weights and activations of a step are copied by LDS-DMA into a ring of NST buffers.
+//  * I8Direct: every wavefront has 32 channels of its own and streams their weights into a ring of
+//    registers; LDS holds only activations. More bytes are in flight on a CU.
+// Either way one barrier per step is all the synchronization there is, and the operands of each
+// half chunk (32 of K) are read from LDS while the products of the half before run.
 //  * Weights lie in tiles of 16 rows in the MFMA's lane order, so copies and reads of them are
 //    contiguous.
-//  * Activations lie as rows of 64 bytes, their four 16-byte pieces permuted by the row
-//    (piece p of row m at p ^ ((m >> 2) & 3)): the 64 lanes of a B read then meet every bank once
+//  * Activations lie in LDS as rows of 128 bytes, their eight 16-byte pieces permuted by the row
+//    (piece p of row m at p ^ ((m >> 1) & 7)): the 64 lanes of a B read then meet every bank once
 //    per quarter (16-byte LDS reads serve lanes 0-3, 12-15, 20-27 of each half together).
 //  * SwiGLU: gate tiles and up tiles alternate, so a lane's 16 sums of a 32x32 block are 8 gate
 //    values and the 8 up values of the same channels.
@@ -22,24 +26,51 @@ namespace moe {
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
 
+// 16 bytes per lane from a buffer into 1 KB of LDS (zeros past the buffer).
+__device__ __forceinline__ void buf_copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff,
+                                           uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)lds, 16, voff, soff, 0, 0);
+}
+
+constexpr int kI8Step = 2 * kI8Chunk;   // K of a step
+
 // WK > 1: WK wavefronts split K, each with a ring of its own, and their sums meet in LDS at the end;
 // there is no barrier in the K loop.
 template <int BM_, int BN_, int WM_, int WN_, int NST_, int WK_ = 1>
 struct I8Tile {
+  static constexpr bool kDirect = false;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, WK = WK_;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * WK * kWave;   // (waves of a group)
   static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;      // 32x32 blocks per wavefront
-  // 1 KB copies of a wavefront per chunk: weight tiles, then 16 activation rows each
-  static constexpr int kOpsB = BN / 16 / kWaves, kOpsA = (BM / 16 + kWaves - 1) / kWaves;
-  static constexpr int kOpsW = kOpsB + kOpsA;
-  static constexpr int kStage = (BM + BN) * kI8Chunk;
+  // 1 KB copies of a wavefront per step: weight tiles of both chunks, then 8 activation rows each
+  static constexpr int kOpsB = BN / 8 / kWaves, kOpsA = BM / 8 / kWaves, kOpsW = kOpsB + kOpsA;
+  static constexpr int kStageA = BN * kI8Step;                    // where a step's activations lie
+  static constexpr int kStage = (BM + BN) * kI8Step;
   static constexpr int kRing = WK * NST * kStage;
   static constexpr int kRed = WK > 1 ? WK * BM * BN * 4 : 0;   // sums of the groups, where the rings were
   static constexpr int kLds = kRing + (BM + BN) * 8;   // + what the epilogue needs per row and channel
-  static_assert(BN / 16 % kWaves == 0, "every wavefront copies the same number of tiles");
+  static_assert(BN / 16 % kWaves == 0 && BM / 8 % kWaves == 0, "the same number of copies each");
   static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "whole blocks");
   static_assert(NST * kOpsW <= 63, "vmcnt range");
   static_assert(WK == 1 || kWaves == 1, "groups of one wavefront");
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+// NST: steps in flight, of activations in LDS and of weights in registers.
+template <int BM_, int BN_, int NST_>
+struct I8Direct {
+  static constexpr bool kDirect = true;
+  static constexpr int BM = BM_, BN = BN_, WM = 1, WN = BN / 32, NST = NST_, WK = 1;
+  static constexpr int kWaves = WN, kThreads = kWaves * kWave;
+  static constexpr int FM = BM / 32, FN = 1;
+  static constexpr int kChunks = 2 * NST;                         // weight chunks in registers
+  static constexpr int kOpsB = 1, kOpsA = BM / 8 / kWaves;        // (kOpsB: unused)
+  static constexpr int kStageA = 0, kStage = BM * kI8Step;
+  static constexpr int kOut = 32 * (BN * 4 + 16);                 // (what the epilogue needs at least)
+  static constexpr int kRing = NST * kStage > kOut ? NST * kStage : kOut, kRed = 0;
+  static constexpr int kLds = kRing + (BM + BN) * 8;
+  static_assert(BM / 8 % kWaves == 0, "the same number of copies each");
+  static_assert(4 * NST - 4 + (NST - 2) * kOpsA <= 63 && NST >= 2, "vmcnt range");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
@@ -161,23 +192,26 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     src_r[i] = (int)src;
   }
   __builtin_amdgcn_sched_barrier(0);
-  // 3. copies of a chunk: operation j < BN / 16 is weight tile j, the others 16 rows each
-  const int KP = i8_pitch(K), CK = KP / kI8Chunk;
-  const int cb = CK * part / TL::WK, C = CK * (part + 1) / TL::WK - cb;   // this group's chunks
+  const int wm = wave % TL::WM, wn = wave / TL::WM;
+  const int l31 = lane & 31, hi = lane >> 5;
+
+  // 3. copies. Steps [db, db + S) of K are this group's; the last step may have one chunk (the
+  // rows' padding is zero: it is multiplied with the weights of the chunk before)
+  const int KP = i8_pitch(K), CK = i8_chunks(K), DK = (CK + 1) / 2;
+  const int db = DK * part / TL::WK, S = DK * (part + 1) / TL::WK - db;
   uint8_t* const ring = lds + part * NST * TL::kStage;
-  // tile or group of 16 rows that copy i of this wavefront takes; a surplus group repeats the last
-  // one (the same bytes to the same place)
-  auto tile_of = [&](int i) { return wave + i * TL::kWaves; };
-  auto rows_of = [&](int i) { return min(wave + i * TL::kWaves, BM / 16 - 1); };
-  // each operation: a 64-bit scalar address that steps through the chunks and a 32-bit offset per
-  // lane (the rows of a routed product lie within 4 GB, a dense one starts at its own rows)
   const int64_t wstep = (int64_t)NT * kI8TileBytes;
-  const int8_t* wbase = wq + ((int64_t)e * CK + cb) * wstep;
-  const int8_t* abase = a + (ROUTED ? 0 : r0 * KP) + cb * kI8Chunk;
-  const int first = ROUTED ? 0 : (int)r0;
+  const int first = ROUTED ? 0 : (int)r0;   // (the rows of a routed product lie within 4 GB)
+  const int8_t* const a0 = a + (int64_t)first * KP;
+  auto tile_of = [&](int i) { return wave + i * TL::kWaves; };   // weight tile of copy i
+  auto rows_of = [&](int i) { return wave + i * TL::kWaves; };   // group of 8 rows of copy i
+  // I8Tile: 64-bit scalar addresses that step through K and a 32-bit offset per lane
+  const int8_t* wbase = wq + ((int64_t)e * CK + 2 * db) * wstep;
+  const int8_t* abase = a0 + db * kI8Step;
+  int wnext = 2 * db;   // chunk at wbase
   uint32_t wvoff[TL::kOpsB], avoff[TL::kOpsA];
 #pragma unroll
-  for (int i = 0; i < TL::kOpsB; ++i) {
+  for (int i = 0; i < (TL::kDirect ? 0 : TL::kOpsB / 2); ++i) {
     // tiles past the last one repeat it; their channels are not stored
     const int j = tile_of(i);
     const int t = GLU ? (j & 1) * HT + min(u0 + (j >> 1), HT - 1) : min(u0 + j, NT - 1);
@@ -187,27 +221,57 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   // the activations out of L2 (64 tokens: 92 -> 81 us); with more row blocks an expert the others
   // find them there (512 tokens with the hint: 122 -> 138 us)
   auto issue_w = [&](int slot) {
-    uint8_t* const st = ring + slot * TL::kStage;
+    const int64_t second = wnext + 1 < CK ? wstep : 0;
 #pragma unroll
     for (int i = 0; i < TL::kOpsB; ++i) {
+      const int half = i / ((TL::kOpsB + 1) / 2), ti = i % ((TL::kOpsB + 1) / 2);
+      const int8_t* const p = (half ? wbase + second : wbase) + wvoff[ti];
+      uint8_t* const to = ring + slot * TL::kStage + half * BN * kI8Chunk + tile_of(ti) * 1024;
       if (once)
-        __builtin_amdgcn_global_load_lds((gptr_t)(wbase + wvoff[i]), (lptr_t)(st + tile_of(i) * 1024), 16, 0, 2);
+        __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)to, 16, 0, 2);
       else
-        __builtin_amdgcn_global_load_lds((gptr_t)(wbase + wvoff[i]), (lptr_t)(st + tile_of(i) * 1024), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)to, 16, 0, 0);
     }
-    wbase += wstep;
+    wbase += 2 * wstep;
+    wnext += 2;
   };
   auto issue_a = [&](int slot) {
-    uint8_t* const st = ring + slot * TL::kStage;
 #pragma unroll
     for (int i = 0; i < TL::kOpsA; ++i)
       __builtin_amdgcn_global_load_lds((gptr_t)(abase + avoff[i]),
-                                       (lptr_t)(st + BN * kI8Chunk + rows_of(i) * 1024), 16, 0, 0);
-    abase += kI8Chunk;
+                                       (lptr_t)(ring + slot * TL::kStage + TL::kStageA + rows_of(i) * 1024), 16, 0, 0);
+    abase += kI8Step;
   };
+  // I8Direct: buffer loads; what lies past the end is out of range (zeros, nothing read), so that
+  // every trip has the same loads in flight. The wavefront's two tiles are the halves of a 32-row
+  // operand.
+  constexpr int kChunks = TL::kDirect ? 2 * NST : 1;
+  const int dt = GLU ? ((l31 >> 4) ? HT : 0) + min(u0 + wave, HT - 1) : min(u0 + 2 * wave + (l31 >> 4), NT - 1);
+  const uint32_t dvoff = (uint32_t)dt * kI8TileBytes + hi * 256 + (l31 & 15) * 16;
+  u32x4_t dw[kChunks][2];
+  auto load_w = [&](int i, int c) {
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(wq + (int64_t)e * CK * wstep, c < CK ? (uint32_t)(CK * wstep) : 0u);
+    const uint32_t soff = c < CK ? (uint32_t)(c * wstep) : 0u;
+    dw[i][0] = once ? buf_load16_nt(r, dvoff, soff) : buf_load16(r, dvoff, soff);
+    dw[i][1] = once ? buf_load16_nt(r, dvoff + 512, soff) : buf_load16(r, dvoff + 512, soff);
+  };
+  const uint32_t abytes = (uint32_t)((ROUTED ? a_rows : (int64_t)live) * KP);
+  auto load_a = [&](int slot, int d) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a0, d < DK ? abytes : 0u);
 #pragma unroll
-  for (int s = 0; s < NST; ++s)
-    if (s < C) issue_w(s);
+    for (int i = 0; i < TL::kOpsA; ++i)
+      buf_copy16(r, ring + slot * TL::kStage + rows_of(i) * 1024, avoff[i], d * kI8Step);
+  };
+
+  if constexpr (TL::kDirect) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) load_w(i, i);
+  } else {
+#pragma unroll
+    for (int s = 0; s < NST; ++s)
+      if (s < S) issue_w(s);
+  }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < kRowsT; ++i) {
@@ -218,51 +282,19 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   lds_barrier();
 #pragma unroll
   for (int i = 0; i < TL::kOpsA; ++i) {
-    const int m = rows_of(i) * 16 + (lane >> 2);
-    const int piece = (lane & 3) ^ ((m >> 2) & 3);
+    const int m = rows_of(i) * 8 + (lane >> 3);
+    const int piece = (lane & 7) ^ ((m >> 1) & 7);
     avoff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
   }
 #pragma unroll
-  for (int s = 0; s < NST; ++s)
-    if (s < C) issue_a(s);
+  for (int s = 0; s < NST; ++s) {
+    if constexpr (TL::kDirect)
+      load_a(s, s);
+    else if (s < S)
+      issue_a(s);
+  }
   __builtin_amdgcn_sched_barrier(0);
 
-  // 4. the K loop
-  const int wm = wave % TL::WM, wn = wave / TL::WM;
-  const int l31 = lane & 31, hi = lane >> 5;
-  // weight block f: tiles 2 f and 2 f + 1 of the wavefront's; piece 2 ks + hi of a row
-  const int wo = (wn * FN * 2 + (l31 >> 4)) * 1024 + (l31 & 15) * 16 + hi * 256;
-  const int ml = wm * FM * 32 + l31;
-  const int ao = BN * kI8Chunk + ml * kI8Chunk;
-  const int p0 = (hi ^ ((ml >> 2) & 3)) * 16;          // ks = 0; ks = 1 is piece ^ 2
-  i32x16_t acc[FN][FM];
-#pragma unroll
-  for (int f = 0; f < FN; ++f)
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[f][m][i] = 0;
-
-  // The operands of each half chunk (32 of K) are read while the products of the half before run:
-  // read right before their products, 1 to 2 wavefronts a SIMD waited for LDS in every half
-  i32x4_t wv[2][FN], av[2][FM];
-  auto read = [&](int h, const uint8_t* st) {
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-      wv[h][f] = *reinterpret_cast<const i32x4_t*>(st + wo + f * 2048 + h * 512);
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-      av[h][m] = *reinterpret_cast<const i32x4_t*>(st + ao + m * 32 * kI8Chunk + (p0 ^ (h * 32)));
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto multiply = [&](int h) {
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-#pragma unroll
-      for (int m = 0; m < FM; ++m)
-        acc[f][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[h][f], av[h][m], acc[f][m], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-  };
   // what the epilogue needs goes out behind the first copies: the scale of a row, scale and bias
   // of a channel
   constexpr int kChT = (BN + TL::kThreads - 1) / TL::kThreads;
@@ -285,38 +317,109 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     }
   }
   __builtin_amdgcn_sched_barrier(0);
-  // (the activations' copies of the first chunks lie behind all their weights')
-  if (C >= NST)
+
+  // 4. the K loop: half chunk h (0..3) of a step multiplies pieces 2 h + hi of the rows with the
+  // same pieces of the weights
+  const int wo = (wn * FN * 2 + (l31 >> 4)) * 1024 + (l31 & 15) * 16 + hi * 256;
+  const int ml = wm * FM * 32 + l31, sw = (ml >> 1) & 7;
+  i32x16_t acc[FN][FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][m][i] = 0;
+  i32x4_t wv[2][FN], av[2][FM];   // operands of the half in hand and of the next
+  auto read = [&](int h, const uint8_t* st) {
+    if constexpr (!TL::kDirect)
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+        wv[h & 1][f] = *reinterpret_cast<const i32x4_t*>(st + (h >> 1) * BN * kI8Chunk + wo + f * 2048 + (h & 1) * 512);
+    const uint8_t* const p = st + TL::kStageA + ml * kI8Step + (((2 * h + hi) ^ sw) << 4);
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+      av[h & 1][m] = *reinterpret_cast<const i32x4_t*>(p + m * 32 * kI8Step);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+        acc[f][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[h & 1][f], av[h & 1][m], acc[f][m], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // the activations' copies of the first steps lie behind all their weights'
+  if (TL::kDirect || S >= NST)
     __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 1) * TL::kOpsA));
   else
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  if (C > 0) read(0, ring);
-  int slot = 0;
-  for (int c = 0; c < C; ++c) {
-    const int next = slot == NST - 1 ? 0 : slot + 1;
-    read(1, ring + slot * TL::kStage);
-    multiply(0);
-    if (c + 1 < C) {
-      // this wavefront has read chunk c, and its copies of chunk c + 1 have landed (those of the
-      // chunks after it may be in flight); the barrier says so for every wavefront
-      if (c + NST > C)
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0) & ~(15 << 8));
-      else if (c < NST - 1)   // in flight behind it: the activations' copies of NST - 2 - c chunks at least
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsA) & ~(15 << 8));
-      else
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsW) & ~(15 << 8));
-      if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      if (c + NST < C) {
-        issue_w(slot);
-        issue_a(slot);
+  if (S > 0) read(0, ring);
+  if constexpr (TL::kDirect) {
+    for (int c0 = 0; c0 < CK; c0 += kChunks) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = c0 + i, h = (i & 1) * 2;
+        if (c >= CK) break;
+        const uint8_t* const st = ring + (i >> 1) * TL::kStage;
+        read(h + 1, st);
+        __builtin_memcpy(&wv[0][0], &dw[i][0], 16);
+        multiply(h);
+        if (i & 1) {
+          // this wavefront has read the step, and its activations of the next have landed (behind
+          // them: the weights of their own trip and of 2 NST - 3 more, the activations of NST - 2
+          // steps; at first the activations of NST - 2 steps at least); the barrier says so for
+          // every wavefront
+          if (c < 2 * NST - 2)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsA) & ~(15 << 8));
+          else
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(4 * NST - 4 + (NST - 2) * TL::kOpsA) & ~(15 << 8));
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          load_a(i >> 1, (c >> 1) + NST);
+          read(0, ring + ((i >> 1) + 1) % NST * TL::kStage);
+        } else {
+          read(2, st);
+        }
+        __builtin_memcpy(&wv[1][0], &dw[i][1], 16);
+        multiply(h + 1);
+        load_w(i, c + kChunks);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      read(0, ring + next * TL::kStage);
     }
-    multiply(1);
-    slot = next;
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));   // no copy into LDS outlives the loop
+  } else {
+    int slot = 0;
+    for (int s = 0; s < S; ++s) {
+      const int next = slot == NST - 1 ? 0 : slot + 1;
+      const uint8_t* const st = ring + slot * TL::kStage;
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        read(h + 1, st);
+        multiply(h);
+      }
+      if (s + 1 < S) {
+        // this wavefront has read the step, and its copies of the next have landed (those of the
+        // steps after it may be in flight); the barrier says so for every wavefront
+        if (s + NST > S)
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm(0) & ~(15 << 8));
+        else if (s < NST - 1)   // behind it: the activations' copies of NST - 2 - s steps at least
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsA) & ~(15 << 8));
+        else
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * TL::kOpsW) & ~(15 << 8));
+        if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + NST < S) {
+          issue_w(slot);
+          issue_a(slot);
+        }
+        read(0, ring + next * TL::kStage);
+      }
+      multiply(3);
+      slot = next;
+    }
   }
 
 #pragma unroll
@@ -509,13 +612,12 @@ int launch_tile(const I8GemmArgs& g, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }
 
-// The tiles. LDS holds three workgroups of I8Mid or I8Wide a CU, one of the others.
-using I8Few = I8Tile<32, 32, 1, 1, 8, 4>;     // few rows: K split over four wavefronts
-using I8Low = I8Tile<32, 64, 1, 1, 6, 4>;
-using I8Half = I8Tile<64, 64, 1, 1, 4, 4>;
-using I8Mid = I8Tile<64, 128, 1, 4, 3>;
-using I8Wide = I8Tile<128, 128, 2, 2, 3>;
-using I8Big = I8Tile<256, 256, 2, 4, 4>;
+using I8Few = I8Tile<32, 32, 1, 1, 4, 4>;     // few rows: K split over four wavefronts
+using I8Low = I8Tile<32, 64, 1, 1, 3, 4>;
+using I8Half = I8Tile<64, 64, 1, 1, 2, 4>;
+using I8Mid = I8Direct<64, 128, 3>;
+using I8Wide = I8Direct<128, 128, 3>;
+using I8Big = I8Tile<256, 256, 2, 4, 2>;
 
 template <class TL>
 int launch_dense(const I8GemmArgs& g, hipStream_t st) {
@@ -533,9 +635,9 @@ int launch_routed(const I8GemmArgs& g, bool glu, hipStream_t st) {
 // Time of a dense product per chunk of K, in ns: a CU goes through ceil(tiles / 256) tiles, `one`
 // ns a chunk where that is one and `each` ns for each of several, as measured at 2880 -> 5760
 // channels and (I8Big) 8192 -> 8192 on 256 CUs. The least of them names the tile: at 64 rows
-// I8Low takes 8.0 us, I8Few 11, I8Half 10, I8Mid 14; at 128 rows I8Half 10.6, I8Low 13.9, I8Mid
-// 15; at 512 rows I8Mid 20, I8Wide 21.5, I8Half 28; at 2048 rows I8Wide 46, I8Big 50, I8Mid 52;
-// 4096 rows of 8192: I8Big 266, I8Wide 306.
+// I8Low takes 7.4 us, I8Few 10.0, I8Half 10.8, I8Mid 15; at 128 rows I8Half 9.6, I8Low 12.9, I8Mid
+// 13.4; at 512 rows I8Mid 17.0, I8Wide 18.6, I8Half 25; at 2048 rows I8Wide 38.8, I8Mid 43.6, I8Big
+// 46.2; 4096 rows of 8192: I8Big 267, I8Wide 302.
 template <class TL>
 double chunk_ns(int64_t rows, int units, double one, double each) {
   const int64_t tiles = (rows + TL::BM - 1) / TL::BM * ((units + TL::BN / 16 - 1) / (TL::BN / 16));
@@ -554,14 +656,14 @@ int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, i
                      out, out_dt, ld_out};
   if (counts) {
     // rows of an expert, padding included: below 64 most experts have one block of I8Mid (256
-    // tokens, 32 rows an expert: gate_up 94 us, I8Wide 99; 512 tokens: 123 and 114 us)
+    // tokens, 32 rows an expert: gate_up 87 us, I8Wide 90; 512 tokens: 114 and 102 us)
     const bool glu = act == MOE_ACT_SWIGLU_OAI;
     return mpad / w->E < 64 ? launch_routed<I8Mid>(g, glu, st) : launch_routed<I8Wide>(g, glu, st);
   }
   const int units = i8_tiles(w->N, w->glu);
-  const double ns[] = {chunk_ns<I8Few>(rows, units, 45, 70),   chunk_ns<I8Low>(rows, units, 78, 100),
-                       chunk_ns<I8Half>(rows, units, 140, 155), chunk_ns<I8Mid>(rows, units, 245, 168),
-                       chunk_ns<I8Wide>(rows, units, 360, 300), chunk_ns<I8Big>(rows, units, 1040, 1040)};
+  const double ns[] = {chunk_ns<I8Few>(rows, units, 45, 68),   chunk_ns<I8Low>(rows, units, 70, 100),
+                       chunk_ns<I8Half>(rows, units, 120, 150), chunk_ns<I8Mid>(rows, units, 215, 147),
+                       chunk_ns<I8Wide>(rows, units, 310, 270), chunk_ns<I8Big>(rows, units, 930, 1025)};
   int best = 0;
   for (int i = 1; i < 6; ++i)
     if (ns[i] < ns[best]) best = i;

@@ -71,7 +71,7 @@ i8_pack_kernel(const int8_t* __restrict__ src, int64_t total, int N, int K, int 
                int8_t* __restrict__ dst) {
   const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (gid >= total) return;
-  const int NT = i8_tiles(N, glu), C = i8_pitch(K) / kI8Chunk;
+  const int NT = i8_tiles(N, glu), C = i8_chunks(K);
   const int l = (int)(gid & 63);
   const int64_t tile = gid >> 6;
   const int t = (int)(tile % NT);
@@ -117,8 +117,7 @@ int launch_quantize(const void* x, int64_t ld, const int32_t* live, int64_t rows
 
 extern "C" int64_t i8_packed_bytes(int E, int N, int K, int glu) {
   if (E < 1 || N < 1 || K < 1 || K > MOE_I8_MAX_K || (glu != 0 && (N & 1))) return -1;
-  return (int64_t)E * moe::i8_tiles(N, glu != 0) * (moe::i8_pitch(K) / moe::kI8Chunk) *
-         moe::kI8TileBytes;
+  return (int64_t)E * moe::i8_tiles(N, glu != 0) * moe::i8_chunks(K) * moe::kI8TileBytes;
 }
 
 extern "C" int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu, int8_t* q_dst,

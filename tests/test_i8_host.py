@@ -38,7 +38,7 @@ def test_packed_bytes_refuses():
 
 
 def test_pitch():
-    assert [_lib.i8_pitch(k) for k in (1, 63, 64, 65, 2880, 1003)] == [64, 64, 64, 128, 2880, 1024]
+    assert [_lib.i8_pitch(k) for k in (1, 127, 128, 129, 2880, 1003)] == [128, 128, 128, 256, 2944, 1024]
 
 
 @no_gpu
