@@ -483,8 +483,8 @@ int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live, int
  * channels come out in their order (gate rows, then up rows).
  *   out   out_dtype [rows][N], ld_out elements from one row to the next (ld_out >= N).
  * i8_linear: the same from plain rows x (as i8_quantize takes them); q_ws (int8 [rows][KP]) and
- * s_ws (f32 [rows]) are scratch that the call may write and leaves without meaning. Calls that
- * can run concurrently need distinct scratch.
+ * s_ws (f32 [rows]) are scratch that the call may write and leaves without meaning (up to four
+ * rows go without). Calls that can run concurrently need distinct scratch. out must not overlap x.
  * Errors: MOE_EINVAL for NULL pointers, rows < 1, E/N/K < 1, unknown dtypes, glu not 0 or 1;
  *         MOE_ESHAPE for E != 1, K > MOE_I8_MAX_K, odd N with glu, a matrix of 2 GB or more,
  *         ld_out < N, ld < K, rows >= 2^31; MOE_EALIGN for aq (q_ws) or w->q not 16-byte aligned,
@@ -503,8 +503,8 @@ int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows, const i8_exp
  * Rows that are padding or ghost are left unwritten, and so is a live row whose a_row entry is
  * outside [0, a_rows).
  * Errors: as mx4_moe_gemm (aq in place of a, also NULL as or w->s), with K <= MOE_I8_MAX_K in
- *         place of K % 32 == 0; MOE_ESHAPE also for MOE_ACT_SWIGLU_OAI with w->glu == 0 and for
- *         an expert of 2 GB or more.
+ *         place of K % 32 == 0; MOE_ESHAPE also for MOE_ACT_SWIGLU_OAI with w->glu == 0, an
+ *         expert of 2 GB or more, and quantized rows (a_rows * KP bytes) of 4 GB or more.
  */
 int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t a_rows,
                 const i8_experts* w, const int32_t* counts, const int32_t* basep, int tile_m,

@@ -488,21 +488,30 @@ def _i8_dtype(dtype, name: str) -> int:
     return code
 
 
-def _i8_call(fn: str, dev: int, stream, *args) -> None:
-    """The C entry point on `stream` (by default the current one of device `dev`), with that
-    device current: tensors of another device than the current one are worked on there."""
+def _i8_call(fn: str, dev: int, *args) -> None:
+    """The C entry point on the current stream of device `dev`, with that device current: tensors of
+    another device than the current one are worked on there."""
     torch = _torch()
     f = _i8_fns.get(fn)
     if f is None:
         f = _i8_fns[fn] = getattr(lib(), fn)
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
         st = f(*args, raw)
     else:
         with torch.cuda.device(dev):
             st = f(*args, raw)
     if st != MOE_OK:
         raise MoeError(fn, st)
+
+
+def _i8_on(stream, t):
+    """Context of a call on a stream other than the current one. Everything in it belongs to that
+    stream, what the call allocates included: scratch that goes back to the allocator when the call
+    returns may then only be handed out to work behind it."""
+    if stream.device != t.device:
+        raise ValueError(f"stream: on {stream.device}, the tensors on {t.device}")
+    return _torch().cuda.stream(stream)
 
 
 def _i8_rows(x, name: str) -> int:
@@ -566,6 +575,9 @@ class I8Experts:
 
     def __init__(self, q, s, bias=None, glu: bool = False, stream=None):
         torch = _torch()
+        if stream is not None:
+            with _i8_on(stream, q):
+                return self.__init__(q, s, bias, glu)
         _check(q, torch.int8, "q")
         if q.dim() == 2:
             q = q.unsqueeze(0)
@@ -585,7 +597,7 @@ class I8Experts:
         if nbytes < 0:
             raise MoeError("i8_pack_experts", MOE_ESHAPE)
         qp = torch.empty(nbytes, dtype=torch.int8, device=q.device)
-        _i8_call("i8_pack_experts", dev, stream, q.data_ptr(), E, N, K, glu, qp.data_ptr())
+        _i8_call("i8_pack_experts", dev, q.data_ptr(), E, N, K, glu, qp.data_ptr())
         self.q, self.s, self.bias, self.dev = qp, s, bias, dev
         self.E, self.N, self.K, self.glu = E, N, K, glu
         self.c = I8ExpertsC(qp.data_ptr(), s.data_ptr(),
@@ -596,10 +608,13 @@ class I8Experts:
     def quantized(cls, w, bias=None, glu: bool = False, stream=None):
         """The stack of bf16 / f16 / f32 weights w [E][N][K] (or [N][K]): every output channel is
         quantized as i8_quantize does a row."""
+        if stream is not None:
+            with _i8_on(stream, w):
+                return cls.quantized(w, bias, glu)
         N, K = w.shape[-2], w.shape[-1]
-        q, s = i8_quantize(w.reshape(-1, K), stream=stream)
+        q, s = i8_quantize(w.reshape(-1, K))
         q = q[:, :K].contiguous().reshape(-1, N, K)
-        return cls(q, s.reshape(-1, N), bias, glu, stream)
+        return cls(q, s.reshape(-1, N), bias, glu)
 
     @property
     def nbytes(self) -> int:
@@ -607,8 +622,11 @@ class I8Experts:
 
 
 def i8_quantize(x, live=None, out=None, stream=None):
-    """Quantized rows of bf16 / f16 / f32 rows x [rows][K] (any row stride): (q int8
+    """Quantized rows of bf16 / f16 / f32 rows x [rows][K] (any row stride from K on): (q int8
     [rows][i8_pitch(K)], s f32 [rows]). Rows with live[r] < 0 are left unwritten."""
+    if stream is not None:
+        with _i8_on(stream, x):
+            return i8_quantize(x, live, out)
     torch = _torch()
     ld = _i8_rows(x, "x")
     code = _i8_dtype(x.dtype, "x")
@@ -622,7 +640,7 @@ def i8_quantize(x, live=None, out=None, stream=None):
         _i8_check(out[0], (rows, i8_pitch(K)), torch.int8, "q", dev)
         _i8_check(out[1], (rows,), torch.float32, "s", dev)
     q, s = out
-    _i8_call("i8_quantize", dev, stream, x.data_ptr(), code, ld,
+    _i8_call("i8_quantize", dev, x.data_ptr(), code, ld,
              None if live is None else live.data_ptr(), rows, K, q.data_ptr(), s.data_ptr())
     return q, s
 
@@ -644,6 +662,9 @@ def _i8_dense_out(out, rows: int, w, out_dtype, x, dev: int):
 def i8_gemm(aq, as_, w: I8Experts, out_dtype=None, out=None, stream=None):
     """Dense product of quantized rows (aq, as_) with the one matrix of w: out [rows][N] in
     out_dtype (bf16 by default) or in `out` (any row stride)."""
+    if stream is not None:
+        with _i8_on(stream, aq):
+            return i8_gemm(aq, as_, w, out_dtype, out)
     torch = _torch()
     rows, dev = aq.shape[0], aq.get_device()
     _i8_weights(w, "w", dev)
@@ -652,15 +673,19 @@ def i8_gemm(aq, as_, w: I8Experts, out_dtype=None, out=None, stream=None):
     if out is None and out_dtype is None:
         out_dtype = torch.bfloat16
     out, code, ld = _i8_dense_out(out, rows, w, out_dtype, aq, dev)
-    _i8_call("i8_gemm", dev, stream, aq.data_ptr(), as_.data_ptr(), rows, w.ref, out.data_ptr(),
+    _i8_call("i8_gemm", dev, aq.data_ptr(), as_.data_ptr(), rows, w.ref, out.data_ptr(),
              code, ld)
     return out
 
 
 def i8_linear(x, w: I8Experts, out_dtype=None, out=None, ws=None, stream=None):
-    """Dense projection of bf16 / f16 / f32 rows x [rows][K] (any row stride), quantized per row
-    on the way: out [rows][N] in out_dtype (x's by default) or in `out`. ws: scratch of
-    i8_row_buffers(rows, K) (allocated if None); concurrent calls need distinct scratch."""
+    """Dense projection of bf16 / f16 / f32 rows x [rows][K] (any row stride from K on),
+    quantized per row on the way: out [rows][N] in out_dtype (x's by default) or in `out`, which
+    must not overlap x. ws: scratch of i8_row_buffers(rows, K) (allocated if None); concurrent
+    calls need distinct scratch."""
+    if stream is not None:
+        with _i8_on(stream, x):
+            return i8_linear(x, w, out_dtype, out, ws)
     torch = _torch()
     ld = _i8_rows(x, "x")
     code = _i8_dtype(x.dtype, "x")
@@ -677,7 +702,7 @@ def i8_linear(x, w: I8Experts, out_dtype=None, out=None, ws=None, stream=None):
     if out is None and out_dtype is None:
         out_dtype = x.dtype
     out, ocode, ldo = _i8_dense_out(out, rows, w, out_dtype, x, dev)
-    _i8_call("i8_linear", dev, stream, x.data_ptr(), code, ld, rows, w.ref, ws[0].data_ptr(),
+    _i8_call("i8_linear", dev, x.data_ptr(), code, ld, rows, w.ref, ws[0].data_ptr(),
              ws[1].data_ptr(), out.data_ptr(), ocode, ldo)
     return out
 
@@ -687,6 +712,10 @@ def i8_moe_gemm(aq, as_, a_row, w: I8Experts, counts, basep, tile_m: int, mpad_m
                 stream=None):
     """mx4_moe_gemm in 8-bit integers over quantized rows (aq, as_) from i8_quantize: f32
     [mpad_max][N], or with MOE_ACT_SWIGLU_OAI (w built with glu) bf16 [mpad_max][N/2]."""
+    if stream is not None:
+        with _i8_on(stream, aq):
+            return i8_moe_gemm(aq, as_, a_row, w, counts, basep, tile_m, mpad_max, act, alpha,
+                               limit, out)
     torch = _torch()
     rows, dev = aq.shape[0], aq.get_device()
     _i8_weights(w, "w", dev)
@@ -703,7 +732,7 @@ def i8_moe_gemm(aq, as_, a_row, w: I8Experts, counts, basep, tile_m: int, mpad_m
         out = torch.empty(shape, dtype=dtype, device=aq.device)
     else:
         _i8_check(out, shape, dtype, "out", dev)
-    _i8_call("i8_moe_gemm", dev, stream, aq.data_ptr(), as_.data_ptr(),
+    _i8_call("i8_moe_gemm", dev, aq.data_ptr(), as_.data_ptr(),
              None if a_row is None else a_row.data_ptr(), rows, w.ref, counts.data_ptr(),
              basep.data_ptr(), tile_m, mpad_max, act, float(alpha), float(limit), out.data_ptr())
     return out
@@ -717,6 +746,10 @@ def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha:
     y [T][D] in y_dtype (f32 by default). `out` may hold preallocated tensors under those keys. ws:
     scratch of i8_row_buffers(T*k, F) (allocated if needed); concurrent calls need distinct
     scratch."""
+    if stream is not None:
+        with _i8_on(stream, x):
+            return i8_moe_decode(logits, x, gate_up, down, k, alpha, limit, want_d, y_dtype, out,
+                                 ws)
     torch = _torch()
     dev = x.get_device()
     _i8_weights(gate_up, "gate_up", dev)
@@ -748,7 +781,7 @@ def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha:
         ws = i8_row_buffers(R, F, x.device)
     if ws is not None:
         q, s = ws[0].data_ptr(), ws[1].data_ptr()
-    _i8_call("i8_moe_decode", dev, stream, logits.data_ptr(), x.data_ptr(), T, E, k, gate_up.ref,
+    _i8_call("i8_moe_decode", dev, logits.data_ptr(), x.data_ptr(), T, E, k, gate_up.ref,
              down.ref, float(alpha), float(limit), o["ids"].data_ptr(), o["w"].data_ptr(),
              o["h"].data_ptr(), q, s, o["d"].data_ptr() if "d" in o else None, o["y"].data_ptr(),
              code)
@@ -777,8 +810,9 @@ def moe_layer(x, logits, gate_up, down, k: int, tile_m: int,
     Returns a dict of every intermediate (device tensors)."""
     if projection not in ("gemm", "gemv", "gemm_mx8", "i8"):
         raise ValueError(f"unknown projection {projection!r}")
-    if (projection == "i8") != (isinstance(gate_up, I8Experts) and isinstance(down, I8Experts)):
-        raise TypeError(f"projection {projection!r} and {type(gate_up).__name__} weights")
+    for name, stack in (("gate_up", gate_up), ("down", down)):
+        if isinstance(stack, I8Experts) != (projection == "i8"):
+            raise TypeError(f"{name}: {type(stack).__name__} in projection {projection!r}")
     T, E = logits.shape
     ids, w = moe_route_topk(logits, k, stream=stream)
     mpad = moe_mpad_max(T, k, E, tile_m)

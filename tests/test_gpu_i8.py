@@ -229,6 +229,69 @@ def test_gemm_dense(rows, N, K):
             assert_out(o, p, r, f"{dt}")
 
 
+@pytest.mark.parametrize("rows,N,K", [(5003, 5003, 129), (5003, 4999, 328), (4090, 4090, 65),
+                                      (4090, 4085, 712), (1030, 2051, 200), (2, 60000, 70)])
+def test_gemm_dense_many_rows_and_channels(rows, N, K):
+    """The tiles of large products (their sums are exact in f32 too: K 2^14 < 2^24)."""
+    log(f"i8_gemm {rows}x{K} -> {N}")
+    q, s, b, W = rand_stack(N + K, 1, N, K)
+    aq, as_ = moe.i8_quantize(torch.randn(rows, K, generator=rng(rows), device="cuda").to(BF16))
+    sums = aq[:, :K].float() @ q[0].float().t().contiguous()
+    p = sums.double() * as_.double()[:, None] * s[0].double()
+    out = moe.i8_gemm(aq, as_, W, out_dtype=F32)
+    assert_out(out, p, p + b[0].double(), "f32")
+    same_bits(moe.i8_gemm(aq, as_, W, out_dtype=BF16), out.to(BF16), "bf16")
+
+
+def test_rows_and_outputs_behind_32_bits():
+    """More rows than one launch takes, their codes past 4 GB; an output past 2^31 elements."""
+    rows, N = (1 << 25) + 5, 9
+    x = torch.randn(rows, 1, generator=rng(1), device="cuda").to(BF16)
+    live = torch.ones(rows, dtype=torch.int32, device="cuda")
+    live[-2] = -1
+    aq, as_ = moe.i8_row_buffers(rows, 1)
+    aq[-2], as_[-2] = 5, 0.5
+    moe.i8_quantize(x, live=live, out=(aq, as_))
+    assert int(aq[-2, 7]) == 5 and float(as_[-2]) == 0.5
+    aq[-2], as_[-2] = 0, 0.0
+    sign = torch.sign(x[:, 0].float())
+    sign[-2] = 0.0
+    assert torch.equal(aq[:, 0], (127 * sign).to(torch.int8)) and not bool(aq[-100:, 1:].any())
+    top = torch.where(sign != 0, x[:, 0].float().abs(), 0.0)
+    same_bits(as_, (top.double() / 127).float(), "scales")
+    w = torch.arange(-4, 5, device="cuda", dtype=torch.int8)[:, None].contiguous()
+    sc = torch.full((N,), 0.5, device="cuda")
+    out = moe.i8_gemm(aq, as_, moe.I8Experts(w, sc))
+    for i in range(N):
+        want = (127 * (i - 4)) * sign.double() * (as_ * 0.5).double()
+        same_bits(out[:, i].contiguous() + 0.0, want.float().to(BF16) + 0.0, f"channel {i}")
+    del x, aq, as_, out, live, sign, top, want
+    rows, N, K = 70001, 32771, 64
+    q, s, b, W = rand_stack(1, 1, N, K)
+    aq, as_ = moe.i8_quantize(torch.randn(rows, K, generator=rng(2), device="cuda").to(BF16))
+    out = moe.i8_gemm(aq, as_, W)
+    tail = moe.i8_gemm(aq[-3:, :].contiguous(), as_[-3:].contiguous(), W)
+    same_bits(out[-3:], tail, "last rows")
+    same_bits(out[:3], moe.i8_gemm(aq[:3].contiguous(), as_[:3].contiguous(), W), "first rows")
+
+
+def test_experts_behind_4_gb_and_the_longest_sums():
+    E, N, K, tokens = 3, 24000, 65536, 5
+    g = rng(4)
+    q = torch.randint(-128, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    s = torch.rand(E, N, generator=g, device="cuda") * 1e-4
+    W = moe.I8Experts(q, s)
+    aq, as_ = moe.i8_quantize(torch.randn(tokens, K, generator=g, device="cuda").to(BF16))
+    cnt, basep, row_tok, mpad = csr([2, 0, 4], 1, 1, tokens)
+    out = moe.i8_moe_gemm(aq, as_, row_tok, W, cnt, basep, 1, mpad)
+    for e, span in ((0, slice(0, 2)), (2, slice(2, 6))):
+        t = row_tok[span].long()
+        for n0 in (0, 11008, N - 992):
+            n = slice(n0, n0 + 992)
+            p, ref = ref_project(aq[t, :K], as_[t], q[e, n], s[e, n], None)
+            assert_out(out[span, n], p, ref, f"expert {e} channels {n0}..")
+
+
 @pytest.mark.parametrize("rows,N,K", [(1, 517, 1003), (3, 64, 64), (16, 100, 200), (17, 100, 200),
                                       (70, 300, 520), (300, 130, 2880)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
@@ -479,6 +542,66 @@ def test_on_another_stream():
     torch.cuda.synchronize()
     same_bits(got, want, "decode")
     same_bits(got2, lin, "linear")
+
+
+def busy(stream):
+    """Some milliseconds of work on the stream."""
+    with torch.cuda.stream(stream):
+        a = torch.randn(4096, 4096, device="cuda")
+        for _ in range(8):
+            a = a @ a * 1e-3
+    return a
+
+
+def test_stream_argument_covers_everything_a_call_does():
+    """What a call allocates, copies or packs on the way stays behind the work of its stream, not of
+    the current one: scratch is not handed out again while the stream still needs it."""
+    K, N, rows = 520, 96, 40
+    wts = torch.randn(N, K, generator=rng(1), device="cuda").to(BF16)
+    x = torch.randn(rows, K, generator=rng(2), device="cuda").to(BF16)
+    W = moe.I8Experts.quantized(wts)
+    want = moe.i8_linear(x, W)
+    aq, as_ = moe.i8_quantize(x)
+    logits, xt, GU, DN = layer(3, 9, 8, 2, 200, 96)
+    want_y = moe.i8_moe_decode(logits, xt, GU[3], DN[3], 2)["y"]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    keep = [busy(side)]
+    W2 = moe.I8Experts.quantized(wts, stream=side)
+    got = moe.i8_linear(x, W2, stream=side)
+    aq2, as2 = moe.i8_quantize(x, stream=side)
+    got_gemm = moe.i8_gemm(aq2, as2, W2, stream=side)
+    y = moe.i8_moe_decode(logits, xt, GU[3], DN[3], 2, stream=side)["y"]
+    for n in (rows * moe.i8_pitch(K), N * K, N * moe.i8_pitch(K), 18 * 128):   # the sizes let go
+        keep += [torch.full((n,), 85, dtype=torch.int8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    same_bits(W2.q, W.q, "packed")
+    same_bits(aq2, aq, "quantized")
+    same_bits(got, want, "linear")
+    same_bits(got_gemm, want, "gemm")
+    same_bits(y, want_y, "decode")
+    assert all(bool((t == 85).all()) for t in keep[1:])
+
+
+def test_two_streams_at_once():
+    """Two calls of every entry point in flight together, each with scratch of its own."""
+    sets = []
+    for i in range(2):
+        logits, x, GU, DN = layer(20 + i, 16, 8, 4, 520, 176)
+        sets.append((logits, x, GU[3], DN[3], torch.cuda.Stream()))
+    want = [(moe.moe_layer(x, lo, gu, dn, 4, 8, projection="i8")["y"],
+             moe.i8_moe_decode(lo, x, gu, dn, 4)["y"]) for lo, x, gu, dn, _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for lo, x, gu, dn, st in sets:
+            with torch.cuda.stream(st):
+                got.append((moe.moe_layer(x, lo, gu, dn, 4, 8, projection="i8")["y"],
+                            moe.i8_moe_decode(lo, x, gu, dn, 4)["y"]))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            same_bits(a[0], b[0], "layer")
+            same_bits(a[1], b[1], "decode")
 
 
 def DN_dense(DN):

@@ -156,6 +156,7 @@ def test_moe_gemm_argument_checks():
     assert call(w=stack(E=1025)) == ESHAPE
     assert call(a_row=None) == ESHAPE                              # fewer rows than the CSR
     assert call(mpad=1 << 31) == ESHAPE
+    assert call(a_rows=1 << 25) == ESHAPE                          # 4 GB of rows of 128 bytes
     assert call(aq=OFF[4]) == EALIGN
     assert call(as_=OFF[2]) == EALIGN
     assert call(out=OFF[2]) == EALIGN
@@ -209,3 +210,8 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         _lib.moe_layer(x, torch.zeros(2, 4), None, None, 1, 1, projection="i8")
     with pytest.raises(ValueError):
         _lib.moe_layer(x, torch.zeros(2, 4), None, None, 1, 1, projection="i4")
+    w = object.__new__(_lib.I8Experts)
+    for projection, stacks in (("i8", (w, None)), ("i8", (None, w)), ("gemm", (w, None)),
+                               ("gemv", (None, w)), ("gemm_mx8", (w, w))):
+        with pytest.raises(TypeError):
+            _lib.moe_layer(x, torch.zeros(2, 4), *stacks, 1, 1, projection=projection)
