@@ -1,4 +1,5 @@
-// i8_moe_decode: the whole 8-bit mixture-of-experts layer of a few tokens in two launches.
+// i8_moe_decode: the whole 8-bit mixture-of-experts layer of a few tokens in two launches (three for
+// more than 16 routed rows).
 //
 // The chain is the one of mx4_moe_decode (PR #3579 "dasLLAMA gpt-oss arc", section "Fused MoE
 // expert chain": stage 1 gate and up rows + bias + activation, stage 2 every routed expert's down

@@ -602,7 +602,7 @@ int launch_tile(const I8GemmArgs& g, hipStream_t st) {
   const int64_t mblocks = ROUTED ? g.mpad / TL::BM + (w->E < g.mpad ? w->E : g.mpad)
                                  : (g.rows + TL::BM - 1) / TL::BM;
   const int64_t grid = (mblocks * nblocks + 7) / 8 * 8;
-  if (grid > 0x7FFFFFFFLL) return MOE_ESHAPE;
+  if (grid * TL::kThreads > 0xFFFFFFFFLL) return MOE_ESHAPE;   // threads of a launch
   constexpr int size = OUT == MOE_F32 ? 4 : 2;
   const int vec = !((uintptr_t)g.out & 15) && g.ld_out * size % 16 == 0 &&
                   (GLU || !w->glu || (w->N / 2) * size % 16 == 0);

@@ -13,6 +13,7 @@
 namespace moe {
 
 constexpr int kI8QuantThreads = 256;
+constexpr int64_t kI8MaxGrid = 1 << 23;   // workgroups of a launch: 2^32 threads are too many
 
 // TPR threads per row (a wavefront or the whole workgroup), NV vectors of 8 values per thread in
 // registers; what a longer row has past TPR * NV * 8 values is read a second time.
@@ -67,9 +68,9 @@ i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __rest
 // K values 64 c .. 64 c + 63 in the lane order of the MFMA operand (lane l: row l % 16, values
 // 16 (l / 16) ..), zeros past N and K.
 __global__ void __launch_bounds__(256)
-i8_pack_kernel(const int8_t* __restrict__ src, int64_t total, int N, int K, int glu,
+i8_pack_kernel(const int8_t* __restrict__ src, int64_t first, int64_t total, int N, int K, int glu,
                int8_t* __restrict__ dst) {
-  const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t gid = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (gid >= total) return;
   const int NT = i8_tiles(N, glu), C = i8_chunks(K);
   const int l = (int)(gid & 63);
@@ -97,20 +98,22 @@ int launch_quantize(const void* x, int64_t ld, const int32_t* live, int64_t rows
   const bool vec = !((uintptr_t)x & 15) && (rows == 1 || (ld * kSize) % 16 == 0);
   // many rows: a wavefront each (4 a workgroup); few rows, or rows that a wavefront does not
   // hold in registers: a workgroup each
-  if (K <= kWave * 8 * 8 && rows >= 1024) {
-    const dim3 grid((unsigned)((rows + 3) / 4));
-    if (vec)
-      launch(i8_quantize_kernel<DT, true, 64, 8>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
+  const bool wave = K <= kWave * 8 * 8 && rows >= 1024;
+  const int64_t per = wave ? 4 : 1;
+  for (int64_t r0 = 0; r0 < rows; r0 += kI8MaxGrid * per) {
+    const int64_t n = rows - r0 < kI8MaxGrid * per ? rows - r0 : kI8MaxGrid * per;
+    const dim3 grid((unsigned)((n + per - 1) / per));
+    auto go = [&](auto kernel) {
+      launch(kernel, grid, dim3(kI8QuantThreads), 0, st, (const void*)((const uint8_t*)x + r0 * ld * kSize),
+             ld, live ? live + r0 : nullptr, n, K, q + r0 * i8_pitch(K), s + r0);
+    };
+    if (wave)
+      vec ? go(i8_quantize_kernel<DT, true, 64, 8>) : go(i8_quantize_kernel<DT, false, 64, 8>);
     else
-      launch(i8_quantize_kernel<DT, false, 64, 8>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
-  } else {
-    const dim3 grid((unsigned)rows);
-    if (vec)
-      launch(i8_quantize_kernel<DT, true, 256, 4>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
-    else
-      launch(i8_quantize_kernel<DT, false, 256, 4>, grid, dim3(256), 0, st, x, ld, live, rows, K, q, s);
+      vec ? go(i8_quantize_kernel<DT, true, 256, 4>) : go(i8_quantize_kernel<DT, false, 256, 4>);
+    if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
   }
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
+  return MOE_OK;
 }
 
 }  // namespace moe
@@ -127,10 +130,13 @@ extern "C" int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu
   if (bytes < 0 || E > MOE_MAX_E) return MOE_ESHAPE;
   if (((uintptr_t)q_dst) & 15) return MOE_EALIGN;
   const int64_t lanes = bytes / 16;
-  if ((lanes + 255) / 256 > 0x7FFFFFFFLL) return MOE_ESHAPE;
-  moe::launch(moe::i8_pack_kernel, dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0,
-              (hipStream_t)stream, q_src, lanes, N, K, glu != 0, q_dst);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
+  for (int64_t first = 0; first < lanes; first += moe::kI8MaxGrid * 256) {
+    const int64_t groups = (lanes - first + 255) / 256;
+    moe::launch(moe::i8_pack_kernel, dim3((unsigned)(groups < moe::kI8MaxGrid ? groups : moe::kI8MaxGrid)),
+                dim3(256), 0, (hipStream_t)stream, q_src, first, lanes, N, K, glu != 0, q_dst);
+    if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
+  }
+  return MOE_OK;
 }
 
 extern "C" int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live,
