@@ -64,31 +64,35 @@ i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __rest
   if (lane == 0) s[r] = z.s;
 }
 
-// One lane per 16 bytes of the packed stack: tile t of chunk c holds rows 16 t .. 16 t + 15 and
-// K values 64 c .. 64 c + 63 in the lane order of the MFMA operand (lane l: row l % 16, values
-// 16 (l / 16) ..), zeros past N and K.
+// A wavefront per tile of the packed stack, a lane per 16 bytes: tile t of chunk c holds rows 16 t ..
+// 16 t + 15 and K values 64 c .. 64 c + 63 in the lane order of the MFMA operand (lane l: row l % 16,
+// values 16 (l / 16) ..), zeros past N and K. A workgroup takes four chunks of a tile, so that it
+// reads whole cache lines of the rows. VEC: rows are 16-byte aligned.
+template <bool VEC>
 __global__ void __launch_bounds__(256)
-i8_pack_kernel(const int8_t* __restrict__ src, int64_t first, int64_t total, int N, int K, int glu,
+i8_pack_kernel(const int8_t* __restrict__ src, int64_t first, int N, int K, int glu,
                int8_t* __restrict__ dst) {
-  const int64_t gid = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (gid >= total) return;
-  const int NT = i8_tiles(N, glu), C = i8_chunks(K);
-  const int l = (int)(gid & 63);
-  const int64_t tile = gid >> 6;
-  const int t = (int)(tile % NT);
-  const int64_t ec = tile / NT;
-  const int c = (int)(ec % C);
-  const int64_t e = ec / C;
+  const int NT = i8_tiles(N, glu), C = i8_chunks(K), quads = (C + 3) / 4;
+  const int64_t item = first + blockIdx.x, eq = item / NT, e = eq / quads;
+  const int t = (int)(item - eq * NT), c = (int)(eq - e * quads) * 4 + (int)(threadIdx.x >> 6);
+  if (c >= C) return;
+  const int l = (int)(threadIdx.x & 63);
   const int n = i8_channel(t, l & 15, N, glu);
   const int k0 = c * kI8Chunk + (l >> 4) * 16;
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (n >= 0) {
     const int8_t* row = src + (e * N + n) * (int64_t)K;
+    if (VEC && k0 + 16 <= K) {
+      v = *reinterpret_cast<const uint4*>(row + k0);
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k0 + i < K) w[i >> 2] |= (uint32_t)(uint8_t)row[k0 + i] << (8 * (i & 3));
+      for (int i = 0; i < 16; ++i)
+        if (k0 + i < K) w[i >> 2] |= (uint32_t)(uint8_t)row[k0 + i] << (8 * (i & 3));
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  *reinterpret_cast<uint4*>(dst + gid * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst + (((e * C + c) * NT + t) * kWave + l) * 16) = v;
 }
 
 template <int DT>
@@ -129,11 +133,12 @@ extern "C" int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu
   const int64_t bytes = i8_packed_bytes(E, N, K, glu);
   if (bytes < 0 || E > MOE_MAX_E) return MOE_ESHAPE;
   if (((uintptr_t)q_dst) & 15) return MOE_EALIGN;
-  const int64_t lanes = bytes / 16;
-  for (int64_t first = 0; first < lanes; first += moe::kI8MaxGrid * 256) {
-    const int64_t groups = (lanes - first + 255) / 256;
-    moe::launch(moe::i8_pack_kernel, dim3((unsigned)(groups < moe::kI8MaxGrid ? groups : moe::kI8MaxGrid)),
-                dim3(256), 0, (hipStream_t)stream, q_src, first, lanes, N, K, glu != 0, q_dst);
+  const int64_t items = (int64_t)E * ((moe::i8_chunks(K) + 3) / 4) * moe::i8_tiles(N, glu != 0);
+  const bool vec = !((uintptr_t)q_src & 15) && K % 16 == 0;
+  for (int64_t first = 0; first < items; first += moe::kI8MaxGrid) {
+    const int64_t n = items - first < moe::kI8MaxGrid ? items - first : moe::kI8MaxGrid;
+    moe::launch(vec ? moe::i8_pack_kernel<true> : moe::i8_pack_kernel<false>, dim3((unsigned)n),
+                dim3(256), 0, (hipStream_t)stream, q_src, first, N, K, glu != 0, q_dst);
     if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
   }
   return MOE_OK;
