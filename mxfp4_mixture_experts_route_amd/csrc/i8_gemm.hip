@@ -39,6 +39,7 @@ constexpr int kI8Step = 2 * kI8Chunk;   // K of a step
 template <int BM_, int BN_, int WM_, int WN_, int NST_, int WK_ = 1>
 struct I8Tile {
   static constexpr bool kDirect = false;
+  static constexpr int kSimd = 1;   // wavefronts a SIMD has registers for, at least
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, WK = WK_;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * WK * kWave;   // (waves of a group)
   static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;      // 32x32 blocks per wavefront
@@ -56,18 +57,22 @@ struct I8Tile {
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
-// NST: steps in flight, of activations in LDS and of weights in registers.
-template <int BM_, int BN_, int NST_>
+// NST: steps in flight, of activations in LDS and of weights in registers. WK > 1: WK such groups of
+// wavefronts split K, so that one group's products cover the other's waits.
+template <int BM_, int BN_, int NST_, int WK_ = 1>
 struct I8Direct {
   static constexpr bool kDirect = true;
-  static constexpr int BM = BM_, BN = BN_, WM = 1, WN = BN / 32, NST = NST_, WK = 1;
-  static constexpr int kWaves = WN, kThreads = kWaves * kWave;
+  // (with registers for two instead of three, 512 tokens: gate_up 103 -> 112 us, down 69 -> 76)
+  static constexpr int kSimd = WK_ > 1 ? 2 : 3;
+  static constexpr int BM = BM_, BN = BN_, WM = 1, WN = BN / 32, NST = NST_, WK = WK_;
+  static constexpr int kWaves = WN, kThreads = kWaves * WK * kWave;
   static constexpr int FM = BM / 32, FN = 1;
   static constexpr int kChunks = 2 * NST;                         // weight chunks in registers
   static constexpr int kOpsB = 1, kOpsA = BM / 8 / kWaves;        // (kOpsB: unused)
   static constexpr int kStageA = 0, kStage = BM * kI8Step;
-  static constexpr int kOut = 32 * (BN * 4 + 16);                 // (what the epilogue needs at least)
-  static constexpr int kRing = NST * kStage > kOut ? NST * kStage : kOut, kRed = 0;
+  static constexpr int kRed = WK > 1 ? WK * BM * BN * 4 : 0;
+  static constexpr int kOut = kRed + (WK > 1 ? BM : 32) * (BN * 4 + 16);   // (for the epilogue)
+  static constexpr int kRing = WK * NST * kStage > kOut ? WK * NST * kStage : kOut;
   static constexpr int kLds = kRing + (BM + BN) * 8;
   static_assert(BM / 8 % kWaves == 0, "the same number of copies each");
   static_assert(4 * NST - 4 + (NST - 2) * kOpsA <= 63 && NST >= 2, "vmcnt range");
@@ -117,7 +122,7 @@ struct I8Blocks {
 };
 
 template <class TL, bool GLU, bool ROUTED, int OUT>
-__global__ void __launch_bounds__(TL::kThreads)
+__global__ void __launch_bounds__(TL::kThreads, TL::kSimd)
 i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
                const int32_t* __restrict__ a_row, int64_t a_rows, const int8_t* __restrict__ wq,
                const float* __restrict__ wsc, const float* __restrict__ bias, int E, int N, int K,
@@ -129,7 +134,8 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   constexpr int kUnits = GLU ? BN / 32 : BN / 16;   // 16-channel units of the workgroup
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wave = TL::WK > 1 ? 0 : wid, part = TL::WK > 1 ? wid : 0;
+  const int wave = TL::WK > 1 ? wid % TL::kWaves : wid;   // in its group
+  const int part = TL::WK > 1 ? wid / TL::kWaves : 0;     // the group
 
   // 1. the item: workgroups are dealt to the 8 XCDs round robin, so item numbers are dealt in 8
   // contiguous shares, and an XCD's L2 sees neighbouring items
@@ -246,22 +252,25 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   // every trip has the same loads in flight. The wavefront's two tiles are the halves of a 32-row
   // operand.
   constexpr int kChunks = TL::kDirect ? 2 * NST : 1;
+  // every group makes the same number of trips (they meet in the barriers)
+  const int cb = TL::WK > 1 ? 2 * db : 0, ce = TL::WK > 1 ? min(CK, 2 * (db + S)) : CK;
+  const int trips = TL::WK == 1 ? CK : 2 * ((DK + TL::WK - 1) / TL::WK);
   const int dt = GLU ? ((l31 >> 4) ? HT : 0) + min(u0 + wave, HT - 1) : min(u0 + 2 * wave + (l31 >> 4), NT - 1);
   const uint32_t dvoff = (uint32_t)dt * kI8TileBytes + hi * 256 + (l31 & 15) * 16;
   u32x4_t dw[kChunks][2];
   auto load_w = [&](int i, int c) {
     const __amdgpu_buffer_rsrc_t r =
-        make_rsrc(wq + (int64_t)e * CK * wstep, c < CK ? (uint32_t)(CK * wstep) : 0u);
-    const uint32_t soff = c < CK ? (uint32_t)(c * wstep) : 0u;
+        make_rsrc(wq + (int64_t)e * CK * wstep, cb + c < ce ? (uint32_t)(CK * wstep) : 0u);
+    const uint32_t soff = cb + c < ce ? (uint32_t)((cb + c) * wstep) : 0u;
     dw[i][0] = once ? buf_load16_nt(r, dvoff, soff) : buf_load16(r, dvoff, soff);
     dw[i][1] = once ? buf_load16_nt(r, dvoff + 512, soff) : buf_load16(r, dvoff + 512, soff);
   };
   const uint32_t abytes = (uint32_t)((ROUTED ? a_rows : (int64_t)live) * KP);
   auto load_a = [&](int slot, int d) {
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(a0, d < DK ? abytes : 0u);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a0, d < S ? abytes : 0u);
 #pragma unroll
     for (int i = 0; i < TL::kOpsA; ++i)
-      buf_copy16(r, ring + slot * TL::kStage + rows_of(i) * 1024, avoff[i], d * kI8Step);
+      buf_copy16(r, ring + slot * TL::kStage + rows_of(i) * 1024, avoff[i], (db + d) * kI8Step);
   };
 
   if constexpr (TL::kDirect) {
@@ -354,15 +363,15 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 1) * TL::kOpsA));
   else
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  if constexpr (TL::WK == 1) __builtin_amdgcn_s_barrier();
+  if constexpr (TL::WK == 1 || TL::kDirect) __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  if (S > 0) read(0, ring);
+  if (S > 0 || TL::kDirect) read(0, ring);
   if constexpr (TL::kDirect) {
-    for (int c0 = 0; c0 < CK; c0 += kChunks) {
+    for (int c0 = 0; c0 < trips; c0 += kChunks) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = c0 + i, h = (i & 1) * 2;
-        if (c >= CK) break;
+        if (c >= trips) break;
         const uint8_t* const st = ring + (i >> 1) * TL::kStage;
         read(h + 1, st);
         __builtin_memcpy(&wv[0][0], &dw[i][0], 16);
@@ -442,7 +451,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
       for (int m = 0; m < FM; ++m)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          red[(((part * FN + f) * FM + m) * 4 + q) * kWave + lane] =
+          red[((((part * TL::kWaves + wave) * FN + f) * FM + m) * 4 + q) * kWave + lane] =
               i32x4_t{acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]};
     lds_barrier();
   }
@@ -450,7 +459,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     if constexpr (TL::WK > 1) {
       i32x4_t s = {0, 0, 0, 0};
 #pragma unroll
-      for (int p = 0; p < TL::WK; ++p) s += red[(((p * FN + f) * FM + m) * 4 + q) * kWave + lane];
+      for (int p = 0; p < TL::WK; ++p) s += red[((((p * TL::kWaves + wave) * FN + f) * FM + m) * 4 + q) * kWave + lane];
       return s;
     } else {
       return i32x4_t{acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]};
@@ -615,6 +624,7 @@ int launch_tile(const I8GemmArgs& g, hipStream_t st) {
 using I8Few = I8Tile<32, 32, 1, 1, 4, 4>;     // few rows: K split over four wavefronts
 using I8Low = I8Tile<32, 64, 1, 1, 3, 4>;
 using I8Half = I8Tile<64, 64, 1, 1, 2, 4>;
+using I8Pair = I8Direct<64, 128, 4, 2>;       // K split over two groups
 using I8Mid = I8Direct<64, 128, 3>;
 using I8Wide = I8Direct<128, 128, 3>;
 using I8Big = I8Tile<256, 256, 2, 4, 2>;
@@ -635,9 +645,10 @@ int launch_routed(const I8GemmArgs& g, bool glu, hipStream_t st) {
 // Time of a dense product per chunk of K, in ns: a CU goes through ceil(tiles / 256) tiles, `one`
 // ns a chunk where that is one and `each` ns for each of several, as measured at 2880 -> 5760
 // channels and (I8Big) 8192 -> 8192 on 256 CUs. The least of them names the tile: at 64 rows
-// I8Low takes 7.4 us, I8Few 10.0, I8Half 10.8, I8Mid 15; at 128 rows I8Half 9.6, I8Low 12.9, I8Mid
-// 13.4; at 512 rows I8Mid 17.0, I8Wide 18.6, I8Half 25; at 2048 rows I8Wide 38.8, I8Mid 43.6, I8Big
-// 46.2; 4096 rows of 8192: I8Big 267, I8Wide 302.
+// I8Low takes 7.0 us, I8Few 10.0, I8Half 10.8, I8Pair 15; at 128 rows I8Half 9.6, I8Pair 11.8, I8Low
+// 12.9; at 256 rows I8Pair 12.2, I8Mid 13.5; at 512 rows I8Mid 17.0, I8Wide 18.6, I8Pair 22, I8Half
+// 25; at 2048 rows I8Wide 38.8, I8Mid 43.6, I8Big 46.2; 4096 rows of 8192: I8Big 267, I8Wide 302;
+// 256 rows of 8192: I8Pair 25.4, I8Mid 30.8.
 template <class TL>
 double chunk_ns(int64_t rows, int units, double one, double each) {
   const int64_t tiles = (rows + TL::BM - 1) / TL::BM * ((units + TL::BN / 16 - 1) / (TL::BN / 16));
@@ -662,17 +673,19 @@ int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, i
   }
   const int units = i8_tiles(w->N, w->glu);
   const double ns[] = {chunk_ns<I8Few>(rows, units, 45, 68),   chunk_ns<I8Low>(rows, units, 70, 100),
-                       chunk_ns<I8Half>(rows, units, 120, 150), chunk_ns<I8Mid>(rows, units, 215, 147),
-                       chunk_ns<I8Wide>(rows, units, 310, 270), chunk_ns<I8Big>(rows, units, 930, 1025)};
+                       chunk_ns<I8Half>(rows, units, 120, 150), chunk_ns<I8Pair>(rows, units, 185, 205),
+                       chunk_ns<I8Mid>(rows, units, 215, 147),  chunk_ns<I8Wide>(rows, units, 310, 270),
+                       chunk_ns<I8Big>(rows, units, 930, 1025)};
   int best = 0;
-  for (int i = 1; i < 6; ++i)
+  for (int i = 1; i < 7; ++i)
     if (ns[i] < ns[best]) best = i;
   switch (best) {
     case 0: return launch_dense<I8Few>(g, st);
     case 1: return launch_dense<I8Low>(g, st);
     case 2: return launch_dense<I8Half>(g, st);
-    case 3: return launch_dense<I8Mid>(g, st);
-    case 4: return launch_dense<I8Wide>(g, st);
+    case 3: return launch_dense<I8Pair>(g, st);
+    case 4: return launch_dense<I8Mid>(g, st);
+    case 5: return launch_dense<I8Wide>(g, st);
     default: return launch_dense<I8Big>(g, st);
   }
 }

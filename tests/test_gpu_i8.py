@@ -230,7 +230,8 @@ def test_gemm_dense(rows, N, K):
 
 
 @pytest.mark.parametrize("rows,N,K", [(5003, 5003, 129), (5003, 4999, 328), (4090, 4090, 65),
-                                      (4090, 4085, 712), (1030, 2051, 200), (2, 60000, 70)])
+                                      (4090, 4085, 712), (1030, 2051, 200), (2, 60000, 70),
+                                      (250, 5700, 64), (250, 5701, 130), (130, 8001, 1000)])
 def test_gemm_dense_many_rows_and_channels(rows, N, K):
     """The tiles of large products (their sums are exact in f32 too: K 2^14 < 2^24)."""
     log(f"i8_gemm {rows}x{K} -> {N}")
@@ -293,7 +294,7 @@ def test_experts_behind_4_gb_and_the_longest_sums():
 
 
 @pytest.mark.parametrize("rows,N,K", [(1, 517, 1003), (3, 64, 64), (16, 100, 200), (17, 100, 200),
-                                      (70, 300, 520), (300, 130, 2880)])
+                                      (70, 300, 520), (300, 130, 2880), (256, 4099, 129)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_linear_is_quantize_then_gemm(rows, N, K, dtype):
     q, s, b, W = rand_stack(N + K, 1, N, K, bias=rows != 16)
