@@ -470,8 +470,8 @@ int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu, int8_t* q
  *         its type is taken, 16-byte aligned rows are read fastest.
  *   live  i32 [rows] or NULL: rows with live[r] < 0 are skipped (q and s left unwritten).
  * Errors: MOE_EINVAL for NULL x/q/s, rows or K < 1, unknown x_dtype; MOE_ESHAPE for
- *         K > MOE_I8_MAX_K, ld < K, rows >= 2^31; MOE_EALIGN for q not 16-byte aligned or x, s
- *         not aligned to their type; MOE_ELAUNCH.
+ *         K > MOE_I8_MAX_K, ld < K, rows >= 2^31; MOE_EALIGN for q not 16-byte aligned or x, s,
+ *         live not aligned to their type; MOE_ELAUNCH.
  */
 int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live, int64_t rows, int K,
                 int8_t* q, float* s, void* stream);

@@ -28,7 +28,7 @@ int check_stack(const i8_experts* w) {
 
 int check_align(const void* aq, const float* as, const i8_experts* w, const void* out, int dt) {
   if ((((uintptr_t)aq) & 15) || (((uintptr_t)w->q) & 15) || (((uintptr_t)as) & 3) ||
-      (((uintptr_t)w->s) & 3) || (w->bias && (((uintptr_t)w->bias) & 3)) ||
+      (((uintptr_t)w->s) & 3) || (((uintptr_t)w->bias) & 3) ||
       (((uintptr_t)out) & (elem_size(dt) - 1)))
     return MOE_EALIGN;
   return MOE_OK;
@@ -65,6 +65,7 @@ extern "C" int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_r
   const int out_dt = glu ? MOE_BF16 : MOE_F32;
   st = check_align(aq, as, w, out, out_dt);
   if (st != MOE_OK) return st;
+  if ((((uintptr_t)a_row) & 3) || (((uintptr_t)counts) & 3) || (((uintptr_t)basep) & 3)) return MOE_EALIGN;
   return moe_launch_i8_gemm(aq, as, a_row, a_rows, w, counts, basep, 0, mpad_max, act, alpha, limit,
                             out, out_dt, glu ? w->N / 2 : w->N, (hipStream_t)stream);
 }

@@ -427,7 +427,8 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
                       const float* __restrict__ hs, int T, int E, int k,
                       const int32_t* __restrict__ ids, const float* __restrict__ w,
                       const int8_t* __restrict__ wq, const float* __restrict__ wsc,
-                      const float* __restrict__ bias, int D, int F, int fast, float* __restrict__ d, void* __restrict__ y, int y_dt) {
+                      const float* __restrict__ bias, int D, int F, int fast,
+                      float* __restrict__ d, void* __restrict__ y, int y_dt) {
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // R quantized rows, or none
   constexpr int kWaves = kI8DownThreads / kWave;
   constexpr int NR = ROWS ? kI8RowsRing : kI8DownRing;
@@ -563,8 +564,8 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
 
 extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, int E, int k,
                              const i8_experts* w_gu, const i8_experts* w_dn, float alpha,
-                             float limit, int32_t* ids, float* w, uint16_t* h, int8_t* q_ws, float* s_ws,
-                             float* d, void* y, int y_dtype, void* stream) {
+                             float limit, int32_t* ids, float* w, uint16_t* h, int8_t* q_ws,
+                             float* s_ws, float* d, void* y, int y_dtype, void* stream) {
   if (!logits || !x || !w_gu || !w_dn || !ids || !w || !h || !y || !w_gu->q || !w_gu->s ||
       !w_dn->q || !w_dn->s || T < 1 || E < 1 || k < 1 || k > E)
     return MOE_EINVAL;
@@ -576,7 +577,8 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
     return MOE_ESHAPE;
   if ((((uintptr_t)x) & 15) || (((uintptr_t)h) & 15) || (((uintptr_t)w_gu->q) & 15) ||
       (((uintptr_t)w_dn->q) & 15) || (((uintptr_t)w_gu->s) & 3) || (((uintptr_t)w_dn->s) & 3) ||
-      (((uintptr_t)logits) & 3) || (d && (((uintptr_t)d) & 3)) ||
+      (((uintptr_t)w_gu->bias) & 3) || (((uintptr_t)w_dn->bias) & 3) || (((uintptr_t)ids) & 3) ||
+      (((uintptr_t)w) & 3) || (((uintptr_t)logits) & 3) || (((uintptr_t)d) & 3) ||
       (((uintptr_t)y) & (y_dtype == MOE_F32 ? 3 : 1)))
     return MOE_EALIGN;
   // launch 1 holds up to T quantized rows of x in LDS, launch 2 those of h where they are few

@@ -149,7 +149,7 @@ extern "C" int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t
   if (!x || !q || !s || rows < 1 || K < 1) return MOE_EINVAL;
   if (x_dtype != MOE_BF16 && x_dtype != MOE_F16 && x_dtype != MOE_F32) return MOE_EINVAL;
   if (K > MOE_I8_MAX_K || ld < K || rows > 0x7FFFFFFFLL) return MOE_ESHAPE;
-  if ((((uintptr_t)q) & 15) || (((uintptr_t)s) & 3) ||
+  if ((((uintptr_t)q) & 15) || (((uintptr_t)s) & 3) || (((uintptr_t)live) & 3) ||
       (((uintptr_t)x) & (x_dtype == MOE_F32 ? 3 : 1)))
     return MOE_EALIGN;
   const hipStream_t st = (hipStream_t)stream;

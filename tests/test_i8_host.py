@@ -74,6 +74,7 @@ def test_quantize_argument_checks():
     assert call(s=OFF[2]) == EALIGN
     assert call(x=OFF[1]) == EALIGN
     assert call(x=OFF[2], dt=F32) == EALIGN
+    assert f(FAKE, BF16, 100, OFF[2], 4, 100, FAKE, FAKE, None) == EALIGN
 
 
 @no_gpu
@@ -161,6 +162,8 @@ def test_moe_gemm_argument_checks():
     assert call(as_=OFF[2]) == EALIGN
     assert call(out=OFF[2]) == EALIGN
     assert call(out=OFF[1], act=SW, w=stack(E=4, glu=1)) == EALIGN
+    for name in ("a_row", "counts", "basep"):
+        assert call(**{name: OFF[2]}) == EALIGN, name
 
 
 @no_gpu
@@ -196,6 +199,10 @@ def test_decode_argument_checks():
     assert call(d=OFF[2]) == EALIGN
     assert call(y=OFF[2]) == EALIGN
     assert call(y=OFF[1], dt=BF16) == EALIGN
+    for name in ("ids", "w"):
+        assert call(**{name: OFF[2]}) == EALIGN, name
+    assert call(gu=stack(bias=0x3002, E=4, N=96, K=100, glu=1)) == EALIGN
+    assert call(dn=stack(bias=0x3002, E=4, N=100, K=48)) == EALIGN
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():
