@@ -15,7 +15,9 @@
 // An expert is read once however many of the tokens picked it. Sums are exact integers, so the
 // results are those of i8_quantize, i8_moe_gemm and moe_combine bit for bit.
 //
-// Bound by the stream of weights: 3 D F bytes of every picked expert.
+// Bound by the stream of weights: 3 D F bytes of every picked expert. At D = F = 2880, k = 4: one
+// token 12.0 + 9.4 us (99.5 MB, 4.6 TB/s); 16 tokens of 32 experts 70 + 4 + 41 us (620 MB, 5.4 TB/s);
+// 5 tokens of 128 experts 51 + 4 + 30 us (470 MB, 5.5 TB/s).
 #include "i8.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"

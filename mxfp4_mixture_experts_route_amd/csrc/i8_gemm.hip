@@ -18,6 +18,11 @@
 //    per quarter (16-byte LDS reads serve lanes 0-3, 12-15, 20-27 of each half together).
 //  * SwiGLU: gate tiles and up tiles alternate, so a lane's 16 sums of a 32x32 block are 8 gate
 //    values and the 8 up values of the same channels.
+//
+// What bounds it: with few rows an expert the stream of weights (32 experts of 5760 x 2880, 64
+// tokens: 80 us, 6.7 TB/s); with more of them what a CU takes in, weights and activations, from L2
+// and beyond (512 tokens: 105 us, matrix cores busy 28 % of the time); in large dense products the
+// matrix cores (4096 rows, 8192 -> 8192: 253 us, 2.2 POPS).
 #include "i8.hpp"
 #include "launch.hpp"
 
@@ -224,8 +229,8 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     wvoff[i] = (uint32_t)t * kI8TileBytes + lane * 16;
   }
   // Weights that no other workgroup reads carry the nontemporal hint, so that they do not push
-  // the activations out of L2 (64 tokens: 92 -> 81 us); with more row blocks an expert the others
-  // find them there (512 tokens with the hint: 122 -> 138 us)
+  // the activations out of L2 (gate_up of 64 tokens: 92 -> 80 us); with more row blocks an expert
+  // the others find them there (256 tokens with the hint everywhere: 89 -> 98 us)
   auto issue_w = [&](int slot) {
     const int64_t second = wnext + 1 < CK ? wstep : 0;
 #pragma unroll
@@ -666,8 +671,8 @@ int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, i
   const I8GemmArgs g{a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
                      out, out_dt, ld_out};
   if (counts) {
-    // rows of an expert, padding included: below 64 most experts have one block of I8Mid (256
-    // tokens, 32 rows an expert: gate_up 87 us, I8Wide 90; 512 tokens: 114 and 102 us)
+    // rows of an expert, padding included: below 64 most experts have one block of I8Mid (gate_up
+    // of 32 experts, 64 tokens: 79 us, I8Wide 88; 256 tokens: 89 and 96; 512 tokens: 115 and 107)
     const bool glu = act == MOE_ACT_SWIGLU_OAI;
     return mpad / w->E < 64 ? launch_routed<I8Mid>(g, glu, st) : launch_routed<I8Wide>(g, glu, st);
   }
