@@ -18,7 +18,7 @@ constexpr int64_t kI8MaxGrid = 1 << 23;   // workgroups of a launch: 2^32 thread
 
 // TPR threads per row (a wavefront or the whole workgroup), NV vectors of 8 values per thread in
 // registers; what a longer row has past TPR * NV * 8 values is read a second time.
-template <int DT, bool VEC, int TPR, int NV>
+template <int DT, int TPR, int NV>
 __global__ void __launch_bounds__(kI8QuantThreads)
 i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __restrict__ live,
                    int64_t rows, int K, int8_t* __restrict__ q, float* __restrict__ s) {
@@ -33,13 +33,13 @@ i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __rest
   for (int i = 0; i < NV; ++i) {
     const int u = lane + i * TPR;
     if (u < V) {
-      load8<DT, VEC>(x, base + (int64_t)u * 8, K - u * 8, v[i]);
+      load8<DT>(x, base + (int64_t)u * 8, K - u * 8, v[i]);
       m = max_abs8(v[i], m);
     }
   }
   for (int u = lane + NV * TPR; u < V; u += TPR) {
     float t[8];
-    load8<DT, VEC>(x, base + (int64_t)u * 8, K - u * 8, t);
+    load8<DT>(x, base + (int64_t)u * 8, K - u * 8, t);
     m = max_abs8(t, m);
   }
   m = wave_umax(m);
@@ -59,7 +59,7 @@ i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __rest
   }
   for (int u = lane + NV * TPR; u < V; u += TPR) {
     float t[8];
-    load8<DT, VEC>(x, base + (int64_t)u * 8, K - u * 8, t);
+    load8<DT>(x, base + (int64_t)u * 8, K - u * 8, t);
     *reinterpret_cast<uint2*>(dst + u * 8) = codes8<DT>(z, t);
   }
   if (lane == 0) s[r] = z.s;
@@ -68,8 +68,7 @@ i8_quantize_kernel(const void* __restrict__ x, int64_t ld, const int32_t* __rest
 // A wavefront per tile of the packed stack, a lane per 16 bytes: tile t of chunk c holds rows 16 t ..
 // 16 t + 15 and K values 64 c .. 64 c + 63 in the lane order of the MFMA operand (lane l: row l % 16,
 // values 16 (l / 16) ..), zeros past N and K. A workgroup takes four chunks of a tile, so that it
-// reads whole cache lines of the rows. VEC: rows are 16-byte aligned.
-template <bool VEC>
+// reads whole cache lines of the rows (32 experts of 5760 x 2880: 176 us, 6.0 TB/s).
 __global__ void __launch_bounds__(256)
 i8_pack_kernel(const int8_t* __restrict__ src, int64_t first, int N, int K, int glu,
                int8_t* __restrict__ dst) {
@@ -83,8 +82,8 @@ i8_pack_kernel(const int8_t* __restrict__ src, int64_t first, int N, int K, int 
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (n >= 0) {
     const int8_t* row = src + (e * N + n) * (int64_t)K;
-    if (VEC && k0 + 16 <= K) {
-      v = *reinterpret_cast<const uint4*>(row + k0);
+    if (k0 + 16 <= K) {
+      v = load16_any(row + k0);
     } else {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -100,7 +99,6 @@ template <int DT>
 int launch_quantize(const void* x, int64_t ld, const int32_t* live, int64_t rows, int K,
                     int8_t* q, float* s, hipStream_t st) {
   constexpr int kSize = DT == MOE_F32 ? 4 : 2;
-  const bool vec = !((uintptr_t)x & 15) && (rows == 1 || (ld * kSize) % 16 == 0);
   // many rows: a wavefront each (4 a workgroup); few rows, or rows that a wavefront does not
   // hold in registers: a workgroup each
   const bool wave = K <= kWave * 8 * 8 && rows >= 1024;
@@ -113,9 +111,9 @@ int launch_quantize(const void* x, int64_t ld, const int32_t* live, int64_t rows
              ld, live ? live + r0 : nullptr, n, K, q + r0 * i8_pitch(K), s + r0);
     };
     if (wave)
-      vec ? go(i8_quantize_kernel<DT, true, 64, 8>) : go(i8_quantize_kernel<DT, false, 64, 8>);
+      go(i8_quantize_kernel<DT, 64, 8>);
     else
-      vec ? go(i8_quantize_kernel<DT, true, 256, 4>) : go(i8_quantize_kernel<DT, false, 256, 4>);
+      go(i8_quantize_kernel<DT, 256, 4>);
     if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
   }
   return MOE_OK;
@@ -135,11 +133,10 @@ extern "C" int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu
   if (bytes < 0 || E > MOE_MAX_E) return MOE_ESHAPE;
   if (((uintptr_t)q_dst) & 15) return MOE_EALIGN;
   const int64_t items = (int64_t)E * ((moe::i8_chunks(K) + 3) / 4) * moe::i8_tiles(N, glu != 0);
-  const bool vec = !((uintptr_t)q_src & 15) && K % 16 == 0;
   for (int64_t first = 0; first < items; first += moe::kI8MaxGrid) {
     const int64_t n = items - first < moe::kI8MaxGrid ? items - first : moe::kI8MaxGrid;
-    moe::launch(vec ? moe::i8_pack_kernel<true> : moe::i8_pack_kernel<false>, dim3((unsigned)n),
-                dim3(256), 0, (hipStream_t)stream, q_src, first, N, K, glu != 0, q_dst);
+    moe::launch(moe::i8_pack_kernel, dim3((unsigned)n), dim3(256), 0, (hipStream_t)stream, q_src,
+                first, N, K, glu != 0, q_dst);
     if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
   }
   return MOE_OK;
