@@ -130,6 +130,9 @@ struct I8Quant {
 
 // 16 bytes at any alignment of the element type, by one load (the memory system takes loads of any
 // alignment: 4346 rows of 5951 f16 values are quantized in 21 us, by elements in 33).
+struct I8Bytes16 {
+  uint8_t b[16];
+};
 __device__ __forceinline__ uint4 load16_any(const void* p) {
   uint4 a;
   __builtin_memcpy(&a, p, sizeof(a));
@@ -212,11 +215,12 @@ __host__ __device__ __forceinline__ int i8_lds_pitch(int KP) {
 __device__ __forceinline__ int i8_swizzle(int m, int off) { return off ^ (((m >> 1) & 7) << 4); }
 
 // A row spread over a wavefront: NV vectors of 8 values per lane, vector i of lane l holding values
-// 8 (64 i + l) .. + 7, zeros past the row. Rows of K % 8 == 0 values, 16-byte aligned.
+// 8 (64 i + l) .. + 7, zeros past the row. TAIL: rows of any length, else of K % 8 == 0 values.
 template <int NV, int DT = MOE_BF16>
 struct I8Row {
   static constexpr int kWords = DT == MOE_F32 ? 8 : 4;   // 32-bit words of a vector
   uint32_t v[NV][kWords];
+  template <bool TAIL>
   __device__ __forceinline__ void load(const void* __restrict__ row, int K) {
     const int lane = (int)(threadIdx.x & 63);
 #pragma unroll
@@ -224,11 +228,23 @@ struct I8Row {
       const int u = i * kWave + lane;
 #pragma unroll
       for (int j = 0; j < kWords; ++j) v[i][j] = 0u;
+      if constexpr (TAIL) {
+        if (u * 8 < K && u * 8 + 8 > K) {   // the vector at the end of the row
+#pragma unroll
+          for (int j = 0; j < 7; ++j)
+            if (u * 8 + j < K) {
+              if constexpr (DT == MOE_F32)
+                v[i][j] = ((const uint32_t*)row)[u * 8 + j];
+              else
+                v[i][j >> 1] |= (uint32_t)((const uint16_t*)row)[u * 8 + j] << (16 * (j & 1));
+            }
+          continue;
+        }
+      }
       if (u * 8 < K) {
-        const uint4* p = (const uint4*)row + u * (kWords / 4);
 #pragma unroll
         for (int j = 0; j < kWords / 4; ++j) {
-          const uint4 t = p[j];
+          const uint4 t = load16_any((const I8Bytes16*)row + u * (kWords / 4) + j);
           v[i][4 * j] = t.x;
           v[i][4 * j + 1] = t.y;
           v[i][4 * j + 2] = t.z;

@@ -99,6 +99,7 @@ __device__ __forceinline__ int route_one(const float* __restrict__ logits, float
 
 // Launch 1: workgroup 0 writes the routing, the others one unit (16 gate and 16 up rows) of a pick
 // each: wavefronts {gate, up} x {halves of K}.
+template <bool TAIL>
 __global__ void __launch_bounds__(kI8DecThreads)
 i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restrict__ x, int E, int k,
                       const int8_t* __restrict__ wq, const float* __restrict__ wsc,
@@ -125,10 +126,10 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
   if (lane < E) lv = logits[lane];
   __builtin_amdgcn_sched_barrier(0);   // the logits come first
   I8Row<kI8DecVec> row;
-  if (E <= kWave) row.load(x, K);
+  if (E <= kWave) row.load<TAIL>(x, K);
   __builtin_amdgcn_sched_barrier(0);
   const int e = __builtin_amdgcn_readfirstlane(route_one(logits, lv, E, k, j, keys[wave]));
-  if (E > kWave) row.load(x, K);       // (the routing of more experts needs the registers)
+  if (E > kWave) row.load<TAIL>(x, K);       // (the routing of more experts needs the registers)
 
   const int C = i8_chunks(K), NT = i8_tiles(N, 1), HT = i8_half_tiles(N, 1);
   const int part = wave & 1, tile = (wave >> 1) ? HT + unit : unit;
@@ -170,6 +171,7 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
 }
 
 // Launch 2: a workgroup owns 16 channels; wavefronts {slots} x {parts of K}.
+template <bool TAIL>
 __global__ void __launch_bounds__(1024)
 i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
                    const int32_t* __restrict__ ids, const float* __restrict__ w,
@@ -186,7 +188,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
   const float wt = w[slot];
   __builtin_amdgcn_sched_barrier(0);   // the id comes first
   I8Row<kI8DecVec> row;
-  row.load(h + (int64_t)slot * F, F);
+  row.load<TAIL>(h + (int64_t)slot * F, F);
   __builtin_amdgcn_sched_barrier(0);
   e = __builtin_amdgcn_readfirstlane(min(max(e, 0), E - 1));
   const int C = i8_chunks(F), NT = i8_tiles(D, 0);
@@ -234,11 +236,12 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
 
 // ---- several tokens --------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(kI8DecThreads, 4)
+template <bool TAIL>
+__global__ void __launch_bounds__(kI8DecThreads, TAIL ? 3 : 4)   // (TAIL spills at four)
 i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restrict__ x, int T,
                          int E, int k, const int8_t* __restrict__ wq,
                          const float* __restrict__ wsc, const float* __restrict__ bias, int N,
-                         int K, float alpha, float limit, int units, int upw, int fast,
+                         int K, float alpha, float limit, int units, int upw, int held,
                          int32_t* __restrict__ ids, float* __restrict__ w,
                          uint16_t* __restrict__ h) {
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // quantized rows
@@ -323,7 +326,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   };
   I8Ring<kI8UpRing> ring;
   I8Row<kI8DecVec> xr;
-  if (!fast) {
+  if (!held) {
     for (int m = wave; m < cnt; m += kWaves) {
       const float s = i8_row_to_lds<MOE_BF16>(x, (int64_t)(list[m] / k) * K, K, rowsq, m, LP, KP);
       if (lane == 0) sx[m] = s;
@@ -333,7 +336,7 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     // a row per wavefront; of a single row every wavefront takes a share of the codes
     const int parts = cnt == 1 ? kWaves : 1, share = cnt == 1 ? wave : 0;
     for (int m = cnt == 1 ? 0 : wave;; m += kWaves) {
-      if (m < cnt) xr.load(x + (int64_t)(list[m] / k) * K, K);
+      if (m < cnt) xr.load<TAIL>(x + (int64_t)(list[m] / k) * K, K);
       if (m + kWaves >= cnt) ring.fill(run(ubase, 0));
       if (m < cnt) {
         const I8Quant z(xr.largest());
@@ -376,35 +379,53 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
 
 // The picked experts of launch 2 in the order of their first routed row, and the rows of each.
 struct I8Picks {
-  int sid[kI8DecMaxR];                         // expert of each routed row
+  alignas(16) int sid[kI8DecMaxR];             // expert of each routed row, -1 past the last
   float sw[kI8DecMaxR];                        // its routing weight
-  int ord[kI8DecMaxR];                         // routed rows, those of an expert together
+  alignas(16) int ord[kI8DecMaxR];             // routed rows, those of an expert together
   int ex[kI8DecMaxR], start[kI8DecMaxR + 1];   // picked experts, their first places in ord
   int picked;
 
   __device__ __forceinline__ void build(const int32_t* __restrict__ ids, const float* __restrict__ w,
                                         int R, int E) {
-    const int tid = (int)threadIdx.x;
+    const int tid = (int)threadIdx.x, quads = (R + 3) / 4;
+    int mine = -1;
     if (tid < R) {
-      sid[tid] = min(max(ids[tid], 0), E - 1);
+      mine = min(max(ids[tid], 0), E - 1);
       sw[tid] = w[tid];
     }
+    if (tid < kI8DecMaxR) sid[tid] = mine;
     lds_barrier();
-    if (tid < R) {   // the first row of the same expert, for now in ord
-      int first = tid;
-      for (int r = R - 1; r >= 0; --r)
-        if (sid[r] == sid[tid]) first = r;
+    if (tid < kI8DecMaxR) {   // the first row of the same expert, for now in ord (none: the largest)
+      int first = INT_MAX;
+      if (tid < R) {
+        first = tid;
+#pragma unroll 4
+        for (int q = 0; q < quads; ++q) {  
+          const int4 s = *reinterpret_cast<const int4*>(sid + 4 * q);
+          if (s.x == mine) first = min(first, 4 * q);
+          if (s.y == mine) first = min(first, 4 * q + 1);
+          if (s.z == mine) first = min(first, 4 * q + 2);
+          if (s.w == mine) first = min(first, 4 * q + 3);
+        }
+      }
       ord[tid] = first;
     }
     lds_barrier();
     int place = 0, rank = 0, firsts = 0;
     if (tid < R) {
       const int first = ord[tid];
-      for (int r = 0; r < R; ++r) {
-        const int f = ord[r];
+      auto count = [&](int f, int r) {
         place += f < first || (f == first && r < tid);
         rank += f == r && r < first;
         firsts += f == r;
+      };
+#pragma unroll 4
+      for (int q = 0; q < quads; ++q) {
+        const int4 f = *reinterpret_cast<const int4*>(ord + 4 * q);
+        count(f.x, 4 * q);
+        count(f.y, 4 * q + 1);
+        count(f.z, 4 * q + 2);
+        count(f.w, 4 * q + 3);
       }
       if (first == tid) {
         ex[rank] = sid[tid];
@@ -423,13 +444,13 @@ struct I8Picks {
 
 // Launch 2 of several tokens. ROWS: the h rows come quantized (hq, hs) and go to the MFMA straight
 // from memory; otherwise (few rows) every workgroup quantizes all of them into LDS first.
-template <bool ROWS>
+template <bool ROWS, bool TAIL>
 __global__ void __launch_bounds__(kI8DownThreads)
 i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__ hq,
                       const float* __restrict__ hs, int T, int E, int k,
                       const int32_t* __restrict__ ids, const float* __restrict__ w,
                       const int8_t* __restrict__ wq, const float* __restrict__ wsc,
-                      const float* __restrict__ bias, int D, int F, int fast,
+                      const float* __restrict__ bias, int D, int F, int held,
                       float* __restrict__ d, void* __restrict__ y, int y_dt) {
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // R quantized rows, or none
   constexpr int kWaves = kI8DownThreads / kWave;
@@ -474,11 +495,11 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
 #pragma unroll
     for (int i = 0; i < NR; ++i) bv[i] = buf_load16(rh, bo, (uint32_t)min(c0 + i, C - 1) * kI8Chunk);
   } else {
-    if (fast) {   // loads return in the order of their issue: the weights go behind the last row
+    if (held) {   // loads return in the order of their issue: the weights go behind the last row
       I8Row<kI8DecVec> hr;
       for (int m = wave;; m += kWaves) {
         const bool last = m + kWaves >= R;
-        if (m < R) hr.load(h + (int64_t)p.ord[m] * F, F);
+        if (m < R) hr.load<TAIL>(h + (int64_t)p.ord[m] * F, F);
         if (last) ring.fill(run(wave));
         if (m < R) {
           const I8Quant z(hr.largest());
@@ -596,32 +617,39 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
     if ((((uintptr_t)q_ws) & 15) || (((uintptr_t)s_ws) & 3)) return MOE_EALIGN;
   }
   const size_t lds1 = (size_t)(T * xrow), lds2 = own_rows ? (size_t)(R * hrow) : 0;
+  // rows that fit in registers, and rows that end inside a vector of 8
+  const int held1 = D <= moe::kI8DecVec * 8 * moe::kWave;
+  const int held2 = F <= moe::kI8DecVec * 8 * moe::kWave;
+  const bool tail1 = D % 8 != 0, tail2 = F % 8 != 0;
+  auto gate_up = tail1 ? moe::i8_decode_gate_up_kernel<true> : moe::i8_decode_gate_up_kernel<false>;
+  auto down = !own_rows ? moe::i8_decode_down_kernel<true, false>
+              : tail2   ? moe::i8_decode_down_kernel<false, true>
+                        : moe::i8_decode_down_kernel<false, false>;
   static bool lds_attr_set[moe::kMaxDevices] = {};   // > 64 KB of LDS: opt in once per device
   const int dslot = moe::device_slot();
   if (dslot < 0 || !lds_attr_set[dslot]) {
-    if (hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_gate_up_kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)moe::kI8DecMaxLds) != hipSuccess ||
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&moe::i8_decode_down_kernel<false>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)moe::kI8DecMaxLds) != hipSuccess)
-      return MOE_ELAUNCH;
+    for (const void* f : {reinterpret_cast<const void*>(&moe::i8_decode_gate_up_kernel<true>),
+                          reinterpret_cast<const void*>(&moe::i8_decode_gate_up_kernel<false>),
+                          reinterpret_cast<const void*>(&moe::i8_decode_down_kernel<false, true>),
+                          reinterpret_cast<const void*>(&moe::i8_decode_down_kernel<false, false>)})
+      if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)moe::kI8DecMaxLds) != hipSuccess)
+        return MOE_ELAUNCH;
     if (dslot >= 0) lds_attr_set[dslot] = true;
   }
   const hipStream_t st = (hipStream_t)stream;
-  const int fast1 = D % 8 == 0 && D <= moe::kI8DecVec * 8 * moe::kWave;
-  const int fast2 = F % 8 == 0 && F <= moe::kI8DecVec * 8 * moe::kWave;
-  if (T == 1 && fast1 && fast2) {
+  if (T == 1 && held1 && held2) {
     const int Cd = moe::i8_chunks(D), Cf = moe::i8_chunks(F);
     // launch 2: 16 wavefronts, or as many as there are slots and chunks for
     int parts = 16 / k;
     while (parts > 1 && Cf < 4 * parts) --parts;
-    moe::launch(moe::i8_one_gate_up_kernel, dim3((unsigned)(1 + k * units)), dim3(moe::kI8DecThreads),
+    moe::launch(tail1 ? moe::i8_one_gate_up_kernel<true> : moe::i8_one_gate_up_kernel<false>,
+                dim3((unsigned)(1 + k * units)), dim3(moe::kI8DecThreads),
                 (size_t)(4 * ((Cd + 1) / 2) * moe::kI8Chunk), st, logits, x, E, k, w_gu->q, w_gu->s,
                 w_gu->bias, N, D, alpha, limit, units, ids, w, h);
     if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
-    moe::launch(moe::i8_one_down_kernel, dim3((unsigned)moe::i8_tiles(D, 0)),
-                dim3((unsigned)(64 * k * parts)),
+    moe::launch(tail2 ? moe::i8_one_down_kernel<true> : moe::i8_one_down_kernel<false>,
+                dim3((unsigned)moe::i8_tiles(D, 0)), dim3((unsigned)(64 * k * parts)),
                 (size_t)(k * parts * ((Cf + parts - 1) / parts) * moe::kI8Chunk), st, h, E, k, parts, ids,
                 w, w_dn->q, w_dn->s, w_dn->bias, D, F, d, y, y_dtype);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
@@ -640,23 +668,23 @@ extern "C" int i8_moe_decode(const float* logits, const uint16_t* x, int64_t T, 
   int upw = 1;
   while (upw < units && live * ((units + upw - 1) / upw) > slots) upw += 2;
   const int groups = (units + upw - 1) / upw;
-  moe::launch(moe::i8_decode_gate_up_kernel, dim3((unsigned)(1 + picks * groups)),
+  moe::launch(gate_up, dim3((unsigned)(1 + picks * groups)),
               dim3(moe::kI8DecThreads), lds1, st, logits, x, (int)T, E, k, w_gu->q, w_gu->s,
-              w_gu->bias, N, D, alpha, limit, units, upw, fast1, ids, w, h);
+              w_gu->bias, N, D, alpha, limit, units, upw, held1, ids, w, h);
   if (hipGetLastError() != hipSuccess) return MOE_ELAUNCH;
   const dim3 grid2((unsigned)moe::i8_tiles(D, 0));
   if (own_rows) {
-    moe::launch(moe::i8_decode_down_kernel<false>, grid2, dim3(moe::kI8DownThreads), lds2, st, h,
+    moe::launch(down, grid2, dim3(moe::kI8DownThreads), lds2, st, h,
                 (const int8_t*)nullptr, (const float*)nullptr, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
-                w_dn->bias, D, F, fast2, d, y, y_dtype);
+                w_dn->bias, D, F, held2, d, y, y_dtype);
   } else {
     // every workgroup of launch 2 would quantize every row, some 2 us for 8 of them: more than 16
     // rows are quantized once, by a launch of its own
     const int qs = i8_quantize(h, MOE_BF16, F, nullptr, R, F, q_ws, s_ws, stream);
     if (qs != MOE_OK) return qs;
-    moe::launch(moe::i8_decode_down_kernel<true>, grid2, dim3(moe::kI8DownThreads), 0, st, h,
+    moe::launch(down, grid2, dim3(moe::kI8DownThreads), 0, st, h,
                 (const int8_t*)q_ws, (const float*)s_ws, (int)T, E, k, ids, w, w_dn->q, w_dn->s,
-                w_dn->bias, D, F, fast2, d, y, y_dtype);
+                w_dn->bias, D, F, held2, d, y, y_dtype);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }

@@ -17,11 +17,11 @@ constexpr int kI8FewRing = 12;                // weight chunks of a wavefront in
 constexpr int kI8FewVec = 8;                  // row vectors per lane in registers (K <= 4096)
 constexpr size_t kI8FewMaxLds = 60 * 1024;    // quantized rows
 
-template <int DT>
+template <int DT, bool TAIL>
 __global__ void __launch_bounds__(kI8FewThreads)
 i8_few_kernel(const void* __restrict__ x, int64_t ld, int rows, const int8_t* __restrict__ wq,
               const float* __restrict__ wsc, const float* __restrict__ bias, int N, int K, int glu,
-              int fast, void* __restrict__ out, int out_dt, int64_t ld_out) {
+              int held, void* __restrict__ out, int out_dt, int64_t ld_out) {
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // the quantized rows
   constexpr int kWaves = kI8FewThreads / kWave;
   constexpr int kSize = DT == MOE_F32 ? 4 : 2;
@@ -40,7 +40,7 @@ i8_few_kernel(const void* __restrict__ x, int64_t ld, int rows, const int8_t* __
   I8Ring<kI8FewRing> ring;
   const int jj = tid & 15, m = tid >> 4, n = i8_channel(unit, jj, N, glu);
   float sc = 0.0f, bi = 0.0f;
-  if (!fast) {
+  if (!held) {
     ring.fill(run(0));
     for (int r = wave; r < rows; r += kWaves) {
       const float s = i8_row_to_lds<DT>(x, r * ld, K, rowsq, r, LP, KP);
@@ -52,7 +52,7 @@ i8_few_kernel(const void* __restrict__ x, int64_t ld, int rows, const int8_t* __
     I8Row<kI8FewVec, DT> xr;
     const int parts = rows == 1 ? kWaves : 1, share = rows == 1 ? wave : 0;
     for (int r = rows == 1 ? 0 : wave;; r += kWaves) {
-      if (r < rows) xr.load((const uint8_t*)x + r * ld * kSize, K);
+      if (r < rows) xr.template load<TAIL>((const uint8_t*)x + r * ld * kSize, K);
       __builtin_amdgcn_sched_barrier(0);
       if (r + kWaves >= rows) ring.fill(run(0));
       if (r < rows) {
@@ -95,19 +95,18 @@ bool moe_i8_few(int64_t rows, const i8_experts* w) {
 
 int moe_launch_i8_few(const void* x, int x_dt, int64_t ld, int rows, const i8_experts* w, void* out,
                       int out_dt, int64_t ld_out, hipStream_t st) {
-  const int size = x_dt == MOE_F32 ? 4 : 2;
-  const int fast = w->K % 8 == 0 && w->K <= moe::kI8FewVec * 8 * moe::kWave &&
-                   !((uintptr_t)x & 15) && (rows == 1 || ld * size % 16 == 0);
+  const int held = w->K <= moe::kI8FewVec * 8 * moe::kWave;   // rows that fit in registers
   const size_t lds = (size_t)rows * moe::i8_lds_pitch(moe::i8_pitch(w->K));
   auto go = [&](auto kernel) {
     moe::launch(kernel, dim3((unsigned)moe::i8_tiles(w->N, w->glu)), dim3(moe::kI8FewThreads), lds,
-                st, x, ld, rows, w->q, w->s, w->bias, w->N, w->K, w->glu, fast, out, out_dt, ld_out);
+                st, x, ld, rows, w->q, w->s, w->bias, w->N, w->K, w->glu, held, out, out_dt, ld_out);
   };
+  const bool tail = w->K % 8 != 0;
   if (x_dt == MOE_BF16)
-    go(moe::i8_few_kernel<MOE_BF16>);
+    tail ? go(moe::i8_few_kernel<MOE_BF16, true>) : go(moe::i8_few_kernel<MOE_BF16, false>);
   else if (x_dt == MOE_F16)
-    go(moe::i8_few_kernel<MOE_F16>);
+    tail ? go(moe::i8_few_kernel<MOE_F16, true>) : go(moe::i8_few_kernel<MOE_F16, false>);
   else
-    go(moe::i8_few_kernel<MOE_F32>);
+    tail ? go(moe::i8_few_kernel<MOE_F32, true>) : go(moe::i8_few_kernel<MOE_F32, false>);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ELAUNCH;
 }
