@@ -655,8 +655,8 @@ int launch_routed(const I8GemmArgs& g, bool glu, hipStream_t st) {
 // 25; at 2048 rows I8Wide 38.8, I8Mid 43.6, I8Big 46.2; 4096 rows of 8192: I8Big 267, I8Wide 302;
 // 256 rows of 8192: I8Pair 25.4, I8Mid 30.8.
 template <class TL>
-double chunk_ns(int64_t rows, int units, double one, double each) {
-  const int64_t tiles = (rows + TL::BM - 1) / TL::BM * ((units + TL::BN / 16 - 1) / (TL::BN / 16));
+double chunk_ns(int64_t rows, int64_t E, int units, double one, double each) {
+  const int64_t tiles = E * ((rows + TL::BM - 1) / TL::BM) * ((units + TL::BN / 16 - 1) / (TL::BN / 16));
   const int64_t rounds = (tiles + 255) / 256;
   return rounds == 1 ? one : (double)rounds * each;
 }
@@ -670,20 +670,32 @@ int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, i
   using namespace moe;
   const I8GemmArgs g{a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
                      out, out_dt, ld_out};
-  if (counts) {
-    // rows of an expert, padding included: below 64 most experts have one block of I8Mid (gate_up
-    // of 32 experts, 64 tokens: 79 us, I8Wide 88; 256 tokens: 89 and 96; 512 tokens: 115 and 107)
-    const bool glu = act == MOE_ACT_SWIGLU_OAI;
-    return mpad / w->E < 64 ? launch_routed<I8Mid>(g, glu, st) : launch_routed<I8Wide>(g, glu, st);
-  }
+  // rows of a product and products: of the experts' rows only their sum is known here, so each is
+  // taken to have the mean (padding included). The many rounds of I8Mid over many experts take 172
+  // ns each. gate_up of 32 experts, 64 tokens: I8Mid 79 us, I8Wide 88; 256 tokens: 89 and 96; 512
+  // tokens: 115 and 107; 2048 tokens: 228 and 195. 10 experts of 87 rows, 2338 -> 69 channels:
+  // I8Few 6.2 us, I8Wide 22.9; 6 of 3 rows, 1331 -> 1105: I8Few 5.4, I8Mid 12.3; 20 of 134 rows,
+  // 1982 -> 2 x 98: I8Half 10.8, I8Wide 19.8; 59 of 130 rows, 573 -> 326: I8Mid 14.2, I8Wide 19.7
+  const bool glu = act == MOE_ACT_SWIGLU_OAI;
+  const int64_t n = counts ? (mpad + w->E - 1) / w->E : rows, E = counts ? w->E : 1;
   const int units = i8_tiles(w->N, w->glu);
-  const double ns[] = {chunk_ns<I8Few>(rows, units, 45, 68),   chunk_ns<I8Low>(rows, units, 70, 100),
-                       chunk_ns<I8Half>(rows, units, 120, 150), chunk_ns<I8Pair>(rows, units, 185, 205),
-                       chunk_ns<I8Mid>(rows, units, 215, 147),  chunk_ns<I8Wide>(rows, units, 310, 270),
-                       chunk_ns<I8Big>(rows, units, 930, 1025)};
+  const double ns[] = {chunk_ns<I8Few>(n, E, units, 45, 68),    chunk_ns<I8Low>(n, E, units, 70, 100),
+                       chunk_ns<I8Half>(n, E, units, 120, 150), chunk_ns<I8Pair>(n, E, units, 185, 205),
+                       chunk_ns<I8Mid>(n, E, units, 215, counts ? 172 : 147),
+                       chunk_ns<I8Wide>(n, E, units, 310, 270), chunk_ns<I8Big>(n, E, units, 930, 1025)};
   int best = 0;
-  for (int i = 1; i < 7; ++i)
+  for (int i = 1; i < (counts ? 6 : 7); ++i)
     if (ns[i] < ns[best]) best = i;
+  if (counts) {
+    switch (best) {
+      case 0: return launch_routed<I8Few>(g, glu, st);
+      case 1: return launch_routed<I8Low>(g, glu, st);
+      case 2: return launch_routed<I8Half>(g, glu, st);
+      case 3: return launch_routed<I8Pair>(g, glu, st);
+      case 4: return launch_routed<I8Mid>(g, glu, st);
+      default: return launch_routed<I8Wide>(g, glu, st);
+    }
+  }
   switch (best) {
     case 0: return launch_dense<I8Few>(g, st);
     case 1: return launch_dense<I8Low>(g, st);
