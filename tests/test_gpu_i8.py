@@ -294,7 +294,8 @@ def test_experts_behind_4_gb_and_the_longest_sums():
 
 
 @pytest.mark.parametrize("rows,N,K", [(1, 517, 1003), (3, 64, 64), (16, 100, 200), (17, 100, 200),
-                                      (70, 300, 520), (300, 130, 2880), (256, 4099, 129)])
+                                      (70, 300, 520), (300, 130, 2880), (256, 4099, 129), (4, 40, 4095),
+                                      (2, 40, 4097), (3, 50, 5), (4, 33, 15001), (5, 33, 15001)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_linear_is_quantize_then_gemm(rows, N, K, dtype):
     q, s, b, W = rand_stack(N + K, 1, N, K, bias=rows != 16)
@@ -382,7 +383,8 @@ ROUTED = {
 
 
 @pytest.mark.parametrize("name", list(ROUTED))
-@pytest.mark.parametrize("F,D", [(24, 100), (176, 520), (161, 64)])
+@pytest.mark.parametrize("F,D", [(24, 100), (176, 520), (161, 64), (700, 131), (1500, 65),
+                                 (2049, 328)])
 def test_moe_gemm(name, F, D):
     counts, tile_m = ROUTED[name]
     log(f"i8_moe_gemm {name} F={F} D={D}")
@@ -458,6 +460,8 @@ DECODE = {
     "popular": (16, 32, 4, 130, 70), "most": (16, 16, 8, 96, 80), "wide": (5, 1024, 8, 65, 17),
     "single": (4, 1, 1, 70, 50), "e65": (7, 65, 3, 333, 95), "large": (2, 8, 2, 2880, 2880),
     "long": (16, 6, 2, 8000, 40), "deep": (3, 5, 2, 40, 9000),
+    "odd1": (1, 27, 4, 1737, 179), "odd3": (3, 30, 5, 619, 946), "odd13": (13, 37, 8, 261, 110),
+    "tiny": (1, 3, 2, 3, 5), "one_wide": (1, 200, 8, 97, 4095),
 }
 
 
