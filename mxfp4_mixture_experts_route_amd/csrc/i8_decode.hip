@@ -35,28 +35,37 @@ constexpr int kI8LdsRows = 16;      // h rows that launch 2 quantizes itself
 constexpr int kI8DecVec = 8;        // row vectors per lane held in registers (K <= 4096)
 constexpr size_t kI8DecMaxLds = 140 * 1024;   // quantized rows in LDS
 
-// The j-th expert (ascending) of those set in a bitmap of E <= 1024 bits, or -1; every lane of
-// the calling wavefront gets it.
-__device__ __forceinline__ int nth_expert(const uint32_t* bits, int j) {
-  const int lane = (int)(threadIdx.x & 63);
-  uint32_t w = lane < MOE_MAX_E / 32 ? bits[lane] : 0u;
-  const int c = __popc(w);
-  int before = c;
+// The experts set in a bitmap of E <= 1024 bits, in ascending order, spread over a wavefront.
+struct I8Picked {
+  uint32_t w;           // the lane's 32 bits
+  int before, upto;     // experts in the lanes before it, and with its own
+  int total;
+
+  __device__ __forceinline__ explicit I8Picked(const uint32_t* bits) {
+    const int lane = (int)(threadIdx.x & 63);
+    w = lane < MOE_MAX_E / 32 ? bits[lane] : 0u;
+    upto = __popc(w);
+    before = -upto;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(before, o);
-    if (lane >= o) before += u;
+    for (int o = 1; o < MOE_MAX_E / 32; o <<= 1) {
+      const int u = __shfl_up(upto, o);
+      if (lane >= o) upto += u;
+    }
+    before += upto;
+    total = __builtin_amdgcn_readlane(upto, MOE_MAX_E / 32 - 1);
   }
-  before -= c;
-  const bool mine = j >= before && j < before + c;
-  int id = 0;
-  if (mine) {
-    for (int i = before; i < j; ++i) w &= w - 1;
-    id = lane * 32 + __ffs((int)w) - 1;
+  // The j-th of them (j < total).
+  __device__ __forceinline__ int nth(int j) const {
+    const bool mine = j >= before && j < upto;   // (one lane: those past the bitmap are empty)
+    int id = 0;
+    if (mine) {
+      uint32_t left = w;
+      for (int i = before; i < j; ++i) left &= left - 1;
+      id = (int)(threadIdx.x & 63) * 32 + __ffs((int)left) - 1;
+    }
+    return __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)__ballot(mine)) - 1);
   }
-  const uint64_t who = __ballot(mine);
-  return who ? __shfl(id, __ffsll((unsigned long long)who) - 1) : -1;
-}
+};
 
 // The routed rows (ascending) whose pick is expert e into list, their number returned to every
 // lane of the calling wavefront; at most one per token.
@@ -304,13 +313,13 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   }
   lds_barrier();
   int* const list = lists[wave];   // a copy per wavefront: no barrier
-  int e = nth_expert(bits, j);
-  if (e < 0) return;               // fewer experts were picked than there could have been
+  const I8Picked picked(bits);
+  if (j >= picked.total) return;   // fewer experts were picked than there could have been
+  const int e = picked.nth(j);
   int cnt = rows_of_expert(sid, R, e, list);
   // the list is written and read by the lanes of one wavefront, whose LDS operations complete in
   // order: only the compiler has to keep them so
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  e = __builtin_amdgcn_readfirstlane(e);
   cnt = __builtin_amdgcn_readfirstlane(cnt);
 
   // 2. rows of x quantized into LDS. Loads return in the order of their issue: the weights go out
@@ -377,71 +386,6 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   }
 }
 
-// The picked experts of launch 2 in the order of their first routed row, and the rows of each.
-struct I8Picks {
-  alignas(16) int sid[kI8DecMaxR];             // expert of each routed row, -1 past the last
-  float sw[kI8DecMaxR];                        // its routing weight
-  alignas(16) int ord[kI8DecMaxR];             // routed rows, those of an expert together
-  int ex[kI8DecMaxR], start[kI8DecMaxR + 1];   // picked experts, their first places in ord
-  int picked;
-
-  __device__ __forceinline__ void build(const int32_t* __restrict__ ids, const float* __restrict__ w,
-                                        int R, int E) {
-    const int tid = (int)threadIdx.x, quads = (R + 3) / 4;
-    int mine = -1;
-    if (tid < R) {
-      mine = min(max(ids[tid], 0), E - 1);
-      sw[tid] = w[tid];
-    }
-    if (tid < kI8DecMaxR) sid[tid] = mine;
-    lds_barrier();
-    if (tid < kI8DecMaxR) {   // the first row of the same expert, for now in ord (none: the largest)
-      int first = INT_MAX;
-      if (tid < R) {
-        first = tid;
-#pragma unroll 4
-        for (int q = 0; q < quads; ++q) {  
-          const int4 s = *reinterpret_cast<const int4*>(sid + 4 * q);
-          if (s.x == mine) first = min(first, 4 * q);
-          if (s.y == mine) first = min(first, 4 * q + 1);
-          if (s.z == mine) first = min(first, 4 * q + 2);
-          if (s.w == mine) first = min(first, 4 * q + 3);
-        }
-      }
-      ord[tid] = first;
-    }
-    lds_barrier();
-    int place = 0, rank = 0, firsts = 0;
-    if (tid < R) {
-      const int first = ord[tid];
-      auto count = [&](int f, int r) {
-        place += f < first || (f == first && r < tid);
-        rank += f == r && r < first;
-        firsts += f == r;
-      };
-#pragma unroll 4
-      for (int q = 0; q < quads; ++q) {
-        const int4 f = *reinterpret_cast<const int4*>(ord + 4 * q);
-        count(f.x, 4 * q);
-        count(f.y, 4 * q + 1);
-        count(f.z, 4 * q + 2);
-        count(f.w, 4 * q + 3);
-      }
-      if (first == tid) {
-        ex[rank] = sid[tid];
-        start[rank] = place;
-      }
-      if (tid == 0) {
-        picked = firsts;
-        start[firsts] = R;
-      }
-    }
-    lds_barrier();
-    if (tid < R) ord[place] = tid;
-    lds_barrier();
-  }
-};
-
 // Launch 2 of several tokens. ROWS: the h rows come quantized (hq, hs) and go to the MFMA straight
 // from memory; otherwise (few rows) every workgroup quantizes all of them into LDS first.
 template <bool ROWS, bool TAIL>
@@ -456,64 +400,83 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   constexpr int kWaves = kI8DownThreads / kWave;
   constexpr int NR = ROWS ? kI8RowsRing : kI8DownRing;
   constexpr int kSums = kI8DecMaxR * kI8TileRows / kI8DownThreads;   // sums of a thread
-  __shared__ I8Picks p;
-  __shared__ float sh[kI8DecMaxR];                   // scale of each h row
+  __shared__ int sid[kI8DecMaxR], lists[kWaves][MOE_DECODE_MAX_T];
+  __shared__ uint32_t bits[MOE_MAX_E / 32];
+  __shared__ float sw[kI8DecMaxR], sh[kI8DecMaxR];   // routing weight and scale of each h row
   __shared__ int acc_s[kI8DecMaxR][kI8TileRows];     // sums of each routed row, then its d (f32)
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int R = T * k, unit = (int)blockIdx.x;
   const int FP = i8_pitch(F), LP = i8_lds_pitch(FP), C = i8_chunks(F), NT = i8_tiles(D, 0);
 
+  // the picked experts
+  int id = 0;
+  if (tid < R) {
+    id = min(max(ids[tid], 0), E - 1);
+    sw[tid] = w[tid];
+    sid[tid] = id;
+    if (ROWS) sh[tid] = hs[tid];
+  }
+  if (tid < MOE_MAX_E / 32) bits[tid] = 0u;
   for (int i = tid; i < R * kI8TileRows; i += kI8DownThreads) (&acc_s[0][0])[i] = 0;
-  if (ROWS && tid < R) sh[tid] = hs[tid];
-  p.build(ids, w, R, E);
-  const int picked = __builtin_amdgcn_readfirstlane(p.picked);
+  lds_barrier();
+  if (tid < R) atomicOr(&bits[id >> 5], 1u << (id & 31));
+  lds_barrier();
+  const I8Picked picked(bits);
 
-  // an item is one picked expert's tile over a segment of K
-  const int segs = (C + NR - 1) / NR, items = picked * segs;
+  // an item is one picked expert's tile over a segment of K: its chunks, the number of its rows
+  // and the lane's row (columns past the rows repeat the last one). Past the last item nothing is
+  // read
+  const int segs = (C + NR - 1) / NR, items = picked.total * segs;
   const uint32_t step = (uint32_t)NT * kI8TileBytes;
-  auto run = [&](int it) {
+  int* const list = lists[wave];
+  auto find = [&](int it, int& rho, int& cnt) {
+    if (it >= items) {
+      rho = cnt = 0;
+      return I8Run{make_rsrc(wq, 0u), 0u, step, 0};
+    }
     const int jx = it / segs, seg = it - jx * segs;
     const int cb = C * seg / segs, ce = C * (seg + 1) / segs;
-    const int e = it < items ? __builtin_amdgcn_readfirstlane(p.ex[jx]) : 0;
+    const int e = picked.nth(jx);
+    cnt = __builtin_amdgcn_readfirstlane(rows_of_expert(sid, R, e, list));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // written and read by one wavefront
+    rho = list[min(col, cnt - 1)];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     return I8Run{make_rsrc(wq + (int64_t)e * C * step, (uint32_t)C * step),
-                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, it < items ? ce - cb : 0};
+                 ((uint32_t)cb * NT + unit) * kI8TileBytes, step, ce - cb};
   };
-  // ROWS: the lane's row and piece of the item's activations, behind which its segment's chunks lie
-  auto rows = [&](int it) {
-    const int jx = min(it, items - 1) / segs;
-    const int m = p.start[jx] + min(col, p.start[jx + 1] - p.start[jx] - 1);
-    return (uint32_t)(p.ord[m] * FP + g * 16);
-  };
+  int rho, cnt;
+  const I8Run first = find(wave, rho, cnt);
   I8Ring<NR> ring;
+  // ROWS: the lane's pieces of its row over the item's chunks
   u32x4_t bv[ROWS ? NR : 1];
   const __amdgpu_buffer_rsrc_t rh = make_rsrc(hq, ROWS ? (uint32_t)(R * FP) : 0u);
   if constexpr (ROWS) {
-    ring.fill(run(wave));
-    const uint32_t bo = rows(wave);
+    ring.fill(first);
     const int c0 = C * (wave % segs) / segs;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) bv[i] = buf_load16(rh, bo, (uint32_t)min(c0 + i, C - 1) * kI8Chunk);
+    for (int i = 0; i < NR; ++i)
+      bv[i] = buf_load16(rh, (uint32_t)(rho * FP + g * 16), (uint32_t)min(c0 + i, C - 1) * kI8Chunk);
   } else {
     if (held) {   // loads return in the order of their issue: the weights go behind the last row
       I8Row<kI8DecVec> hr;
       for (int m = wave;; m += kWaves) {
         const bool last = m + kWaves >= R;
-        if (m < R) hr.load<TAIL>(h + (int64_t)p.ord[m] * F, F);
-        if (last) ring.fill(run(wave));
+        if (m < R) hr.load<TAIL>(h + (int64_t)m * F, F);
+        if (last) ring.fill(first);
         if (m < R) {
           const I8Quant z(hr.largest());
           hr.store_codes(z, rowsq, m, LP, FP, 0, 1);
-          if (lane == 0) sh[p.ord[m]] = z.s;
+          if (lane == 0) sh[m] = z.s;
         }
         if (last) break;
       }
     } else {
       for (int m = wave; m < R; m += kWaves) {
-        const float s = i8_row_to_lds<MOE_BF16>(h, (int64_t)p.ord[m] * F, F, rowsq, m, LP, FP);
-        if (lane == 0) sh[p.ord[m]] = s;
+        const float s = i8_row_to_lds<MOE_BF16>(h, (int64_t)m * F, F, rowsq, m, LP, FP);
+        if (lane == 0) sh[m] = s;
       }
-      ring.fill(run(wave));
+      ring.fill(first);
     }
     lds_barrier();
   }
@@ -526,19 +489,18 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
     const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
     dsc[i] = dbi[i] = 0.0f;
     if (r < R && n < D) {
-      const int64_t cg = (int64_t)p.sid[r] * D + n;
+      const int64_t cg = (int64_t)sid[r] * D + n;
       dsc[i] = wsc[cg];
       if (bias) dbi[i] = bias[cg];
     }
   }
 
   for (int it = wave; it < items; it += kWaves) {
-    const int jx = it / segs, seg = it - jx * segs;
-    const int cnt = p.start[jx + 1] - p.start[jx], m0 = p.start[jx];
-    const I8Run next = run(it + kWaves);
+    int rho_next, cnt_next;
+    const I8Run next = find(it + kWaves, rho_next, cnt_next);
     i32x4_t acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
     if constexpr (ROWS) {
-      const uint32_t bo = rows(it + kWaves);
+      const uint32_t bo = (uint32_t)(rho_next * FP + g * 16);
       const int cn = C * ((it + kWaves) % segs) / segs;
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
@@ -553,15 +515,15 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
         bv[i] = buf_load16(rh, bo, (uint32_t)min(cn + i, C - 1) * kI8Chunk);
       }
     } else {
-      const int mb = m0 + min(col, cnt - 1);
-      ring.take(rowsq + mb * LP, mb, C * seg / segs, C - 1, next, acc, acc1);
+      ring.take(rowsq + rho * LP, rho, C * (it % segs) / segs, C - 1, next, acc, acc1);
     }
     acc += acc1;
     if (col < cnt) {
-      const int rho = p.ord[m0 + col];
 #pragma unroll
       for (int i = 0; i < 4; ++i) atomicAdd(&acc_s[rho][4 * g + i], acc[i]);   // exact integers
     }
+    rho = rho_next;
+    cnt = cnt_next;
   }
   lds_barrier();
 
@@ -578,7 +540,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   if (tid < T * kI8TileRows && n < D) {
     const int t = tid >> 4;
     float yv = 0.0f;
-    for (int s = 0; s < k; ++s) yv = fmaf(p.sw[t * k + s], __int_as_float(acc_s[t * k + s][jj]), yv);
+    for (int s = 0; s < k; ++s) yv = fmaf(sw[t * k + s], __int_as_float(acc_s[t * k + s][jj]), yv);
     store_elem(y, (int64_t)t * D + n, yv, y_dt);
   }
 }
