@@ -4,6 +4,8 @@
 
 #include <hip/hip_fp16.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
@@ -201,10 +203,20 @@ __device__ __forceinline__ float i8_swiglu(float gate, float up, float alpha, fl
   return __builtin_isunordered(gate, up) ? __uint_as_float(0x7FC00000u) : h;
 }
 
+// The largest value of the wavefront's lanes, by moves between lanes inside the vector ALU (rows of
+// 16, then their last lanes into the rows behind): six dependent steps of LDS shuffles cost several
+// times as much, and stand in the way of whatever waits for the value.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t m) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-  return m;
+  auto step = [&](auto ctrl, auto rows) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+  };
+  step(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());   // row_shr:1
+  step(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());   // row_shr:2
+  step(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());   // row_shr:4
+  step(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());   // row_shr:8
+  step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());   // row_bcast:15
+  step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());   // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)m, kWave - 1);
 }
 
 // LDS pitch of a quantized row: an odd multiple of 128 bytes, so that with the 16-byte pieces of

@@ -95,11 +95,80 @@ __device__ __forceinline__ void codes_of_part(const I8Row<kI8DecVec>& row, int c
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read by the same wavefront
 }
 
+// The first k <= E <= 64 N experts of a token in the order of rank_key, lane r holding the r-th; v[j]
+// of a lane is the logit of expert 64 j + lane. Each round takes the largest key's high word over
+// the wavefront and the lowest id that has it.
+template <int N>
+__device__ __forceinline__ int wave_pick(const float (&v)[N], int E, int k) {
+  const int lane = (int)(threadIdx.x & 63);
+  uint32_t key[N];   // NaN: 1 (below the word of -inf), taken or absent: 0
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    key[j] = j * kWave + lane < E ? max((uint32_t)(rank_key(v[j], 0) >> 32), 1u) : 0u;
+  int mine = 0;
+  for (int r = 0; r < k; ++r) {
+    uint32_t top = key[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) top = max(top, key[j]);
+    top = wave_umax(top);
+    int id = 0;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j) {
+      const uint64_t who = __ballot(key[j] == top);
+      if (who) id = j * kWave + __ffsll((unsigned long long)who) - 1;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (id == j * kWave + lane) key[j] = 0u;
+    if (lane == r) mine = id;
+  }
+  return mine;
+}
+
+// Logits of one token for wave_pick.
+template <int N>
+__device__ __forceinline__ void load_logits(const float* __restrict__ row, int E, float (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int e = j * kWave + (int)(threadIdx.x & 63);
+    v[j] = e < E ? row[e] : 0.0f;
+  }
+}
+
+// Experts of all routed rows into sid and the bitmap, a token per wavefront; the logits of all of a
+// wavefront's tokens are loaded together.
+template <int N>
+__device__ __forceinline__ void route_tokens(const float* __restrict__ logits, int T, int E, int k,
+                                             int* sid, uint32_t* bits) {
+  constexpr int kWaves = kI8DecThreads / kWave, kEach = (MOE_DECODE_MAX_T + kWaves - 1) / kWaves;
+  const int lane = (int)(threadIdx.x & 63);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  float v[kEach][N];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    load_logits(logits + (size_t)min(wave + i * kWaves, T - 1) * E, E, v[i]);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int t = wave + i * kWaves;
+    if (t >= T) continue;
+    const int id = wave_pick(v[i], E, k);
+    if (lane < k) {
+      sid[t * k + lane] = id;
+      atomicOr(&bits[id >> 5], 1u << (id & 31));
+    }
+  }
+}
+
 // The expert of pick j of the token, the same on every lane.
 __device__ __forceinline__ int route_one(const float* __restrict__ logits, float lv, int E, int k,
                                          int j, uint64_t* keys) {
   const int lane = (int)(threadIdx.x & 63);
   if (E <= kWave) return rank_pick(wave_rank_keys(rank_key(lv, lane), keys, E), j);
+  if (E <= 2 * kWave) {
+    float v[2];
+    load_logits(logits, E, v);
+    return __builtin_amdgcn_readlane(wave_pick(v, E, j + 1), j);
+  }
   int my_id;
   float my_v;
   wave_topk(logits, E, k, my_id, my_v);
@@ -256,7 +325,6 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // quantized rows
   constexpr int kWaves = kI8DecThreads / kWave;
   __shared__ int sid[kI8DecMaxR], lists[kWaves][MOE_DECODE_MAX_T];
-  __shared__ uint64_t keys[kWaves][kWave];
   __shared__ float sx[MOE_DECODE_MAX_T];
   __shared__ uint32_t bits[MOE_MAX_E / 32];
   __shared__ i32x4_t red[2][kWaves][kWave];
@@ -281,24 +349,10 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
   // 1. routing
   if (tid < MOE_MAX_E / 32) bits[tid] = 0u;
   lds_barrier();
-  if (E <= kWave) {   // a logit per lane, the rows of all of a wavefront's tokens loaded together
-    float lv[MOE_DECODE_MAX_T / kWaves];
-#pragma unroll
-    for (int i = 0; i < MOE_DECODE_MAX_T / kWaves; ++i) {
-      const int t = wave + i * kWaves;
-      lv[i] = 0.0f;
-      if (t < T && lane < E) lv[i] = logits[(size_t)t * E + lane];
-    }
-#pragma unroll
-    for (int i = 0; i < MOE_DECODE_MAX_T / kWaves; ++i) {
-      const int t = wave + i * kWaves;
-      if (t >= T) continue;
-      const int rank = wave_rank_keys(rank_key(lv[i], lane), keys[wave], E);
-      if (rank < k) {
-        sid[t * k + rank] = lane;
-        atomicOr(&bits[lane >> 5], 1u << (lane & 31));
-      }
-    }
+  if (E <= kWave) {
+    route_tokens<1>(logits, T, E, k, sid, bits);
+  } else if (E <= 2 * kWave) {
+    route_tokens<2>(logits, T, E, k, sid, bits);
   } else {
     for (int t = wave; t < T; t += kWaves) {
       int my_id;

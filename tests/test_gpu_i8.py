@@ -484,6 +484,39 @@ def test_decode_is_the_chain_bit_for_bit(name):
     assert "d" not in o2
 
 
+@pytest.mark.parametrize("T", [1, 6, 16])
+@pytest.mark.parametrize("E", [7, 64, 65, 128, 129, 300])
+def test_decode_routes_ties_and_odd_logits_as_the_router(T, E):
+    """Equal logits, zeros of both signs, infinities and NaN: fewer numbers than picks among them.
+    The experts that are computed are those that are written."""
+    k, D, F = 6, 64, 32
+    g = rng(E + T)
+    logits = torch.randint(-2, 3, (T, E), generator=g, device="cuda").float()
+    logits[logits == 0] *= -1.0
+    odd = torch.tensor([float("nan"), float("inf"), float("-inf"), 0.0, -0.0, float("nan")],
+                       device="cuda")
+    logits[:, :6] = odd
+    logits[0, 3:] = float("nan")
+    if T > 2:
+        logits[1] = float("-inf")
+        logits[2] = float("nan")
+    x = torch.randn(T, D, generator=g, device="cuda").to(BF16)
+    GU, DN = rand_stack(1, E, 2 * F, D, glu=True), rand_stack(2, E, D, F)
+    o = moe.i8_moe_decode(logits, x, GU[3], DN[3], k)
+    ids, _ = moe.moe_route_topk(logits, k)
+    assert torch.equal(o["ids"], ids)
+    aq, as_ = moe.i8_quantize(x)
+    for t in range(T):
+        for r in range(k):
+            e = int(ids[t, r])
+            one = moe.I8Experts(GU[0][e], GU[1][e].contiguous(), GU[2][e].contiguous(), glu=True)
+            want = moe.i8_moe_gemm(aq[t:t + 1].contiguous(), as_[t:t + 1].contiguous(), None, one,
+                                   torch.ones(1, dtype=torch.int32, device="cuda"),
+                                   torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1, 1,
+                                   SWIGLU, ALPHA, LIMIT)
+            same_bits(o["h"][t * k + r], want[0], f"token {t} slot {r} expert {e}")
+
+
 @pytest.mark.parametrize("T,E,k,D,F,tile_m", [(1, 4, 2, 64, 64, 1), (9, 8, 3, 100, 70, 4),
                                              (200, 6, 2, 130, 90, 16), (600, 3, 2, 96, 48, 16)])
 def test_layer_against_the_definition(T, E, k, D, F, tile_m):
