@@ -473,15 +473,24 @@ def mx4_moe_decode_persistent_static(logits, x, gate_up: MX4Experts, down: MX4Ex
 # 8-bit integer projections
 # ---------------------------------------------------------------------------------------------
 
+# These calls take a few microseconds on the GPU, so that the host's share shows: what they need on
+# every call is kept in module names, and a check looks into its details when it has failed.
+_i8_torch = None
 _i8_codes = {}   # torch dtype -> moe_dtype
 _i8_fns = {}     # C entry points by name
 
 
+def _i8_load():
+    global _i8_torch
+    torch = _torch()
+    _i8_codes.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32})
+    _i8_torch = torch
+    return torch
+
+
 def _i8_dtype(dtype, name: str) -> int:
-    if not _i8_codes:
-        torch = _torch()
-        _i8_codes.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16,
-                          torch.float32: MOE_F32})
+    if _i8_torch is None:
+        _i8_load()
     code = _i8_codes.get(dtype)
     if code is None:
         raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
@@ -491,7 +500,7 @@ def _i8_dtype(dtype, name: str) -> int:
 def _i8_call(fn: str, dev: int, *args) -> None:
     """The C entry point on the current stream of device `dev`, with that device current: tensors of
     another device than the current one are worked on there."""
-    torch = _torch()
+    torch = _i8_torch
     f = _i8_fns.get(fn)
     if f is None:
         f = _i8_fns[fn] = getattr(lib(), fn)
@@ -514,26 +523,30 @@ def _i8_on(stream, t):
     return _torch().cuda.stream(stream)
 
 
-def _i8_rows(x, name: str) -> int:
-    """Checks a device matrix of rows whose elements are contiguous; returns its row pitch in
-    elements."""
+def _i8_rows(x, name: str):
+    """Checks a device matrix of rows whose elements are contiguous; returns its rows, their
+    length and their pitch in elements."""
     if not x.is_cuda:
         raise TypeError(f"{name}: expected a device tensor")
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix of rows, got shape {tuple(x.shape)}")
-    rows, n = x.shape
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a matrix of rows, got shape {tuple(shape)}")
+    rows, n = shape
     ld, one = x.stride()
-    if n > 1 and one != 1:
+    if one != 1 and n > 1:
         raise ValueError(f"{name}: expected rows of contiguous elements")
     if rows < 2:
-        return n
+        return rows, n, n
     if ld < n:
         raise ValueError(f"{name}: rows overlap (stride {ld} of {n} elements)")
-    return ld
+    return rows, n, ld
 
 
 def _i8_check(t, shape, dtype, name: str, dev: int) -> None:
     """Checks a contiguous tensor of this shape and type on device number `dev`."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+            and t.is_cuda):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -542,8 +555,7 @@ def _i8_check(t, shape, dtype, name: str, dev: int) -> None:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on device {t.get_device()}, the others on {dev}")
+    raise ValueError(f"{name}: on device {t.get_device()}, the others on {dev}")
 
 
 def _i8_weights(w, name: str, dev: int) -> None:
@@ -574,7 +586,7 @@ class I8Experts:
     on the current stream; holds its tensors alive."""
 
     def __init__(self, q, s, bias=None, glu: bool = False, stream=None):
-        torch = _torch()
+        torch = _i8_torch or _i8_load()
         if stream is not None:
             with _i8_on(stream, q):
                 return self.__init__(q, s, bias, glu)
@@ -627,10 +639,9 @@ def i8_quantize(x, live=None, out=None, stream=None):
     if stream is not None:
         with _i8_on(stream, x):
             return i8_quantize(x, live, out)
-    torch = _torch()
-    ld = _i8_rows(x, "x")
+    rows, K, ld = _i8_rows(x, "x")
     code = _i8_dtype(x.dtype, "x")
-    rows, K = x.shape
+    torch = _i8_torch
     dev = x.get_device()
     if live is not None:
         _i8_check(live, (rows,), torch.int32, "live", dev)
@@ -651,9 +662,9 @@ def _i8_dense_out(out, rows: int, w, out_dtype, x, dev: int):
         return out, _i8_dtype(out_dtype, "out"), w.N
     if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
-    ld = _i8_rows(out, "out")
-    if out.shape != (rows, w.N):
-        raise ValueError(f"out: expected shape {(rows, w.N)}, got {tuple(out.shape)}")
+    n_rows, n, ld = _i8_rows(out, "out")
+    if n_rows != rows or n != w.N:
+        raise ValueError(f"out: expected shape {(rows, w.N)}, got {(n_rows, n)}")
     if out.get_device() != dev:
         raise ValueError(f"out: on device {out.get_device()}, the others on {dev}")
     return out, _i8_dtype(out.dtype, "out"), ld
@@ -665,7 +676,7 @@ def i8_gemm(aq, as_, w: I8Experts, out_dtype=None, out=None, stream=None):
     if stream is not None:
         with _i8_on(stream, aq):
             return i8_gemm(aq, as_, w, out_dtype, out)
-    torch = _torch()
+    torch = _i8_torch or _i8_load()
     rows, dev = aq.shape[0], aq.get_device()
     _i8_weights(w, "w", dev)
     _i8_check(aq, (rows, i8_pitch(w.K)), torch.int8, "aq", dev)
@@ -686,10 +697,9 @@ def i8_linear(x, w: I8Experts, out_dtype=None, out=None, ws=None, stream=None):
     if stream is not None:
         with _i8_on(stream, x):
             return i8_linear(x, w, out_dtype, out, ws)
-    torch = _torch()
-    ld = _i8_rows(x, "x")
+    rows, K, ld = _i8_rows(x, "x")
     code = _i8_dtype(x.dtype, "x")
-    rows, K = x.shape
+    torch = _i8_torch
     dev = x.get_device()
     _i8_weights(w, "w", dev)
     if K != w.K:
@@ -716,7 +726,7 @@ def i8_moe_gemm(aq, as_, a_row, w: I8Experts, counts, basep, tile_m: int, mpad_m
         with _i8_on(stream, aq):
             return i8_moe_gemm(aq, as_, a_row, w, counts, basep, tile_m, mpad_max, act, alpha,
                                limit, out)
-    torch = _torch()
+    torch = _i8_torch or _i8_load()
     rows, dev = aq.shape[0], aq.get_device()
     _i8_weights(w, "w", dev)
     _i8_check(aq, (rows, i8_pitch(w.K)), torch.int8, "aq", dev)
@@ -750,7 +760,7 @@ def i8_moe_decode(logits, x, gate_up: I8Experts, down: I8Experts, k: int, alpha:
         with _i8_on(stream, x):
             return i8_moe_decode(logits, x, gate_up, down, k, alpha, limit, want_d, y_dtype, out,
                                  ws)
-    torch = _torch()
+    torch = _i8_torch or _i8_load()
     dev = x.get_device()
     _i8_weights(gate_up, "gate_up", dev)
     _i8_weights(down, "down", dev)
