@@ -9,15 +9,15 @@
 //    takes the j-th picked expert with the tokens that picked it, quantizes their rows of x into
 //    LDS and runs one gate tile and its up tile over them; h is written in routed-row order, in
 //    bf16. One extra workgroup writes ids and w.
-//  * Launch 2: a workgroup owns 16 channels of every token. It quantizes the h rows into LDS, runs
-//    the tile of each picked expert once over the rows of the tokens that picked it, and sums the
-//    slots of each token in slot order.
+//  * Launch 2: a workgroup owns 16 channels of every token. It quantizes the h rows into LDS (more
+//    than 16 are quantized by a launch between), runs the tile of each picked expert once over the
+//    rows of the tokens that picked it, and sums the slots of each token in slot order.
 // An expert is read once however many of the tokens picked it. Sums are exact integers, so the
 // results are those of i8_quantize, i8_moe_gemm and moe_combine bit for bit.
 //
 // Bound by the stream of weights: 3 D F bytes of every picked expert. At D = F = 2880, k = 4: one
-// token 12.0 + 9.4 us (99.5 MB, 4.6 TB/s); 16 tokens of 32 experts 70 + 4 + 41 us (620 MB, 5.4 TB/s);
-// 5 tokens of 128 experts 51 + 4 + 30 us (470 MB, 5.5 TB/s).
+// token 11.7 + 9.0 us (99.5 MB, 4.8 TB/s); 16 tokens of 32 experts 70 + 4 + 40 us (620 MB, 5.4 TB/s);
+// 5 tokens of 128 experts 48 + 4 + 27 us (470 MB, 6.0 TB/s).
 #include "i8.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"
