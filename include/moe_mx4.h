@@ -483,8 +483,8 @@ int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live, int
  * channels come out in their order (gate rows, then up rows).
  *   out   out_dtype [rows][N], ld_out elements from one row to the next (ld_out >= N).
  * i8_linear: the same from plain rows x (as i8_quantize takes them); q_ws (int8 [rows][KP]) and
- * s_ws (f32 [rows]) are scratch that the call may write and leaves without meaning (up to four
- * rows go without). Calls that can run concurrently need distinct scratch. out must not overlap x.
+ * s_ws (f32 [rows]) are scratch that the call may write and leaves without meaning (a few
+ * rows may go without). Calls that can run concurrently need distinct scratch. out must not overlap x.
  * Errors: MOE_EINVAL for NULL pointers, rows < 1, E/N/K < 1, unknown dtypes, glu not 0 or 1;
  *         MOE_ESHAPE for E != 1, K > MOE_I8_MAX_K, odd N with glu, a matrix of 2 GB or more,
  *         ld_out < N, ld < K, rows >= 2^31; MOE_EALIGN for aq (q_ws) or w->q not 16-byte aligned,

@@ -15,7 +15,7 @@ namespace moe {
 constexpr int kI8FewThreads = 256;
 constexpr int kI8FewRing = 12;                // weight chunks of a wavefront in flight
 constexpr int kI8FewVec = 8;                  // row vectors per lane in registers (K <= 4096)
-constexpr size_t kI8FewMaxLds = 60 * 1024;    // quantized rows
+constexpr int64_t kI8FewMaxRows = 8, kI8FewMaxValues = 24 * 1024;
 
 template <int DT, bool TAIL>
 __global__ void __launch_bounds__(kI8FewThreads)
@@ -86,11 +86,12 @@ i8_few_kernel(const void* __restrict__ x, int64_t ld, int rows, const int8_t* __
 
 }  // namespace moe
 
-// Whether a product of `rows` rows is taken by moe_launch_i8_few. Quantizing the rows costs every
-// workgroup some 2 us for each four of them, a launch of its own 4 us.
+// Whether a product of `rows` rows is taken by moe_launch_i8_few. Every workgroup quantizes all the
+// rows, four at a time, against a launch of its own for that (calls in a loop, us, here and there):
+// 2880 -> 5760 channels 4 rows 7.3 / 9.1, 8 rows 8.4 / 9.8, 16 rows 11.0 / 9.7; 4096 -> 8192 6 rows
+// 10.2 / 11.0, 8 rows 11.8 / 11.0; 8000 -> 128 2 rows 11.8 / 11.7, 4 rows 12.5 / 11.8.
 bool moe_i8_few(int64_t rows, const i8_experts* w) {
-  return rows <= 4 &&
-         (size_t)rows * moe::i8_lds_pitch(moe::i8_pitch(w->K)) <= moe::kI8FewMaxLds;
+  return rows <= moe::kI8FewMaxRows && rows * w->K <= moe::kI8FewMaxValues;
 }
 
 int moe_launch_i8_few(const void* x, int x_dt, int64_t ld, int rows, const i8_experts* w, void* out,

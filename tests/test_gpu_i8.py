@@ -295,7 +295,9 @@ def test_experts_behind_4_gb_and_the_longest_sums():
 
 @pytest.mark.parametrize("rows,N,K", [(1, 517, 1003), (3, 64, 64), (16, 100, 200), (17, 100, 200),
                                       (70, 300, 520), (300, 130, 2880), (256, 4099, 129), (4, 40, 4095),
-                                      (2, 40, 4097), (3, 50, 5), (4, 33, 15001), (5, 33, 15001)])
+                                      (2, 40, 4097), (3, 50, 5), (4, 33, 15001), (5, 33, 15001),
+                                      (8, 40, 3000), (8, 40, 3100), (7, 70, 2001), (5, 33, 4097),
+                                      (6, 33, 4095), (9, 40, 64), (1, 20, 24576), (1, 20, 24577)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_linear_is_quantize_then_gemm(rows, N, K, dtype):
     q, s, b, W = rand_stack(N + K, 1, N, K, bias=rows != 16)
