@@ -108,7 +108,8 @@ def check_quantize(x, q, s, what):
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("rows,K", [(1, 1), (3, 63), (5, 64), (4, 65), (7, 1003), (9, 2880),
-                                    (1030, 2880), (1025, 100), (3, 8200), (1024, 4100), (2, 65536)])
+                                    (1030, 2880), (1025, 100), (3, 8200), (1024, 4100), (2, 65536),
+                                    (2051, 2880), (2049, 100), (2050, 4096), (2050, 4097)])
 def test_quantize_bit_exact(rows, K, dtype):
     log(f"i8_quantize {rows}x{K} {dtype}")
     x = rand_rows(rows * 7 + K, rows, K, dtype)
