@@ -299,6 +299,8 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     const int m = rows_of(i) * 8 + (lane >> 3);
     const int piece = (lane & 7) ^ ((m >> 1) & 7);
     avoff[i] = (uint32_t)max(src_s[m] - first, 0) * (uint32_t)KP + piece * 16;
+    // no row: past any buffer, so that nothing is read
+    if (TL::kDirect && src_s[m] < 0) avoff[i] = 0xFFFFFFF0u;
   }
 #pragma unroll
   for (int s = 0; s < NST; ++s) {
