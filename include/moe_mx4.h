@@ -447,8 +447,8 @@ typedef struct {
   int glu;
 } i8_experts;
 
-/* Bytes of the tiled layout, or -1 for E, N or K < 1, K > MOE_I8_MAX_K, or odd N with glu.
- * Host-only. */
+/* Bytes of the tiled layout, or -1 for E, N or K < 1, K > MOE_I8_MAX_K, odd N with glu, or bytes
+ * past 63 bits. Host-only. */
 int64_t i8_packed_bytes(int E, int N, int K, int glu);
 
 /*

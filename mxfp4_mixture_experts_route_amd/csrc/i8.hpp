@@ -26,9 +26,10 @@ __host__ __device__ __forceinline__ int i8_pitch(int K) { return (K + 127) & ~12
 __host__ __device__ __forceinline__ int i8_chunks(int K) { return (K + kI8Chunk - 1) / kI8Chunk; }
 
 // Weight tiles of an expert: N rows in tiles of 16, or, packed for SwiGLU, each half (gate rows,
-// up rows) in tiles of its own, so that a gate tile and its up tile always match row for row.
+// up rows) in tiles of its own, so that a gate tile and its up tile always match row for row. Up to
+// N = 2^31 - 1 (N >= 1, >= 2 for SwiGLU) nothing here leaves 32 bits.
 __host__ __device__ __forceinline__ int i8_half_tiles(int N, int glu) {
-  return ((glu ? N / 2 : N) + kI8TileRows - 1) / kI8TileRows;
+  return ((glu ? N / 2 : N) - 1) / kI8TileRows + 1;
 }
 __host__ __device__ __forceinline__ int i8_tiles(int N, int glu) {
   return i8_half_tiles(N, glu) * (glu ? 2 : 1);

@@ -124,7 +124,8 @@ int launch_quantize(const void* x, int64_t ld, const int32_t* live, int64_t rows
 
 extern "C" int64_t i8_packed_bytes(int E, int N, int K, int glu) {
   if (E < 1 || N < 1 || K < 1 || K > MOE_I8_MAX_K || (glu != 0 && (N & 1))) return -1;
-  return (int64_t)E * moe::i8_tiles(N, glu != 0) * moe::i8_chunks(K) * moe::kI8TileBytes;
+  const int64_t each = (int64_t)moe::i8_tiles(N, glu != 0) * moe::i8_chunks(K) * moe::kI8TileBytes;
+  return E <= INT64_MAX / each ? E * each : -1;
 }
 
 extern "C" int i8_pack_experts(const int8_t* q_src, int E, int N, int K, int glu, int8_t* q_dst,
