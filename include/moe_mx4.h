@@ -487,8 +487,9 @@ int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live, int
  * rows may go without). Calls that can run concurrently need distinct scratch. out must not overlap x.
  * Errors: MOE_EINVAL for NULL pointers, rows < 1, E/N/K < 1, unknown dtypes, glu not 0 or 1;
  *         MOE_ESHAPE for E != 1, K > MOE_I8_MAX_K, odd N with glu, a matrix of 2 GB or more,
- *         ld_out < N, ld < K, rows >= 2^31; MOE_EALIGN for aq (q_ws) or w->q not 16-byte aligned,
- *         or other pointers not aligned to their type; MOE_ELAUNCH.
+ *         ld_out < N, ld < K, rows >= 2^31, or a product whose tiles take 2^32 threads or
+ *         more (a thread has at least 4 outputs of a tile); MOE_EALIGN for aq (q_ws) or w->q not
+ *         16-byte aligned, or other pointers not aligned to their type; MOE_ELAUNCH.
  */
 int i8_gemm(const int8_t* aq, const float* as, int64_t rows, const i8_experts* w, void* out,
             int out_dtype, int64_t ld_out, void* stream);
@@ -504,7 +505,8 @@ int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows, const i8_exp
  * outside [0, a_rows).
  * Errors: as mx4_moe_gemm (aq in place of a, also NULL as or w->s), with K <= MOE_I8_MAX_K in
  *         place of K % 32 == 0; MOE_ESHAPE also for MOE_ACT_SWIGLU_OAI with w->glu == 0, an
- *         expert of 2 GB or more, and quantized rows (a_rows * KP bytes) of 4 GB or more.
+ *         expert of 2 GB or more, quantized rows (a_rows * KP bytes) of 4 GB or more, and a
+ *         product too large for one launch (as i8_gemm).
  */
 int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t a_rows,
                 const i8_experts* w, const int32_t* counts, const int32_t* basep, int tile_m,

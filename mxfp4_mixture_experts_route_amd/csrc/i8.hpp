@@ -35,6 +35,13 @@ __host__ __device__ __forceinline__ int i8_tiles(int N, int glu) {
   return i8_half_tiles(N, glu) * (glu ? 2 : 1);
 }
 
+// Rows that a product quantizes before it starts: values of type dt, ld from one row to the next.
+struct I8Plain {
+  const void* x;
+  int dt;
+  int64_t ld;
+};
+
 // Channel of row r of tile t, or -1 in the padding of a tile.
 __device__ __forceinline__ int i8_channel(int t, int r, int N, int glu) {
   if (!glu) {

@@ -1,11 +1,13 @@
 // C ABI entry points of the 8-bit integer projections: host-side argument checks, then the
-// launch. Every check runs before anything is enqueued; on failure nothing is enqueued.
+// launch. Every check runs before anything is enqueued, the product's own limits included (i8_linear
+// quantizes behind them); a call that is refused has enqueued nothing.
 #include "i8.hpp"
 
-int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, int64_t a_rows,
-                       const i8_experts* w, const int32_t* counts, const int32_t* basep,
-                       int64_t rows, int64_t mpad, int act, float alpha, float limit, void* out,
-                       int out_dt, int64_t ld_out, hipStream_t stream);
+int moe_launch_i8_gemm(const moe::I8Plain* plain, const int8_t* a, const float* as,
+                       const int32_t* a_row, int64_t a_rows, const i8_experts* w,
+                       const int32_t* counts, const int32_t* basep, int64_t rows, int64_t mpad,
+                       int act, float alpha, float limit, void* out, int out_dt, int64_t ld_out,
+                       hipStream_t stream);
 
 bool moe_i8_few(int64_t rows, const i8_experts* w);
 int moe_launch_i8_few(const void* x, int x_dt, int64_t ld, int rows, const i8_experts* w, void* out,
@@ -44,8 +46,8 @@ extern "C" int i8_gemm(const int8_t* aq, const float* as, int64_t rows, const i8
   if (w->E != 1 || ld_out < w->N || rows > 0x7FFFFFFFLL) return MOE_ESHAPE;
   st = check_align(aq, as, w, out, out_dtype);
   if (st != MOE_OK) return st;
-  return moe_launch_i8_gemm(aq, as, nullptr, rows, w, nullptr, nullptr, rows, rows, MOE_ACT_NONE,
-                            0.0f, 0.0f, out, out_dtype, ld_out, (hipStream_t)stream);
+  return moe_launch_i8_gemm(nullptr, aq, as, nullptr, rows, w, nullptr, nullptr, rows, rows,
+                            MOE_ACT_NONE, 0.0f, 0.0f, out, out_dtype, ld_out, (hipStream_t)stream);
 }
 
 extern "C" int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row,
@@ -66,8 +68,8 @@ extern "C" int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_r
   st = check_align(aq, as, w, out, out_dt);
   if (st != MOE_OK) return st;
   if ((((uintptr_t)a_row) & 3) || (((uintptr_t)counts) & 3) || (((uintptr_t)basep) & 3)) return MOE_EALIGN;
-  return moe_launch_i8_gemm(aq, as, a_row, a_rows, w, counts, basep, 0, mpad_max, act, alpha, limit,
-                            out, out_dt, glu ? w->N / 2 : w->N, (hipStream_t)stream);
+  return moe_launch_i8_gemm(nullptr, aq, as, a_row, a_rows, w, counts, basep, 0, mpad_max, act,
+                            alpha, limit, out, out_dt, glu ? w->N / 2 : w->N, (hipStream_t)stream);
 }
 
 extern "C" int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows,
@@ -85,9 +87,8 @@ extern "C" int i8_linear(const void* x, int x_dtype, int64_t ld, int64_t rows,
   if (moe_i8_few(rows, w))
     return moe_launch_i8_few(x, x_dtype, ld, (int)rows, w, out, out_dtype, ld_out,
                              (hipStream_t)stream);
-  st = i8_quantize(x, x_dtype, ld, nullptr, rows, w->K, q_ws, s_ws, stream);
-  if (st != MOE_OK) return st;
-  return moe_launch_i8_gemm(q_ws, s_ws, nullptr, rows, w, nullptr, nullptr, rows, rows,
+  const moe::I8Plain plain{x, x_dtype, ld};
+  return moe_launch_i8_gemm(&plain, q_ws, s_ws, nullptr, rows, w, nullptr, nullptr, rows, rows,
                             MOE_ACT_NONE, 0.0f, 0.0f, out, out_dtype, ld_out,
                             (hipStream_t)stream);
 }

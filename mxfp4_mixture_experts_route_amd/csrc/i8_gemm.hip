@@ -587,6 +587,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
 }
 
 struct I8GemmArgs {
+  const I8Plain* plain;   // the rows before quantization, or NULL: a and as hold them quantized
   const int8_t* a;
   const float* as;
   const int32_t* a_row;
@@ -622,6 +623,11 @@ int launch_tile(const I8GemmArgs& g, hipStream_t st) {
   constexpr int size = OUT == MOE_F32 ? 4 : 2;
   const int vec = !((uintptr_t)g.out & 15) && g.ld_out * size % 16 == 0 &&
                   (GLU || !w->glu || (w->N / 2) * size % 16 == 0);
+  if (!ROUTED && g.plain) {   // behind every check, so that a refused call has enqueued nothing
+    const int qs = i8_quantize(g.plain->x, g.plain->dt, g.plain->ld, nullptr, g.rows, w->K,
+                               const_cast<int8_t*>(g.a), const_cast<float*>(g.as), st);
+    if (qs != MOE_OK) return qs;
+  }
   launch(i8_gemm_kernel<TL, GLU, ROUTED, OUT>, dim3((unsigned)grid), dim3(TL::kThreads), TL::kLds, st,
          g.a, g.as, g.a_row, g.a_rows, w->q, w->s, w->bias, w->E, w->N, w->K, w->glu, g.counts,
          g.basep, g.rows, g.mpad, (int)nblocks, g.alpha, g.limit, g.out, g.ld_out, vec);
@@ -665,12 +671,13 @@ double chunk_ns(int64_t rows, int64_t E, int units, double one, double each) {
 
 }  // namespace moe
 
-int moe_launch_i8_gemm(const int8_t* a, const float* as, const int32_t* a_row, int64_t a_rows,
-                       const i8_experts* w, const int32_t* counts, const int32_t* basep,
-                       int64_t rows, int64_t mpad, int act, float alpha, float limit, void* out,
-                       int out_dt, int64_t ld_out, hipStream_t st) {
+int moe_launch_i8_gemm(const moe::I8Plain* plain, const int8_t* a, const float* as,
+                       const int32_t* a_row, int64_t a_rows, const i8_experts* w,
+                       const int32_t* counts, const int32_t* basep, int64_t rows, int64_t mpad,
+                       int act, float alpha, float limit, void* out, int out_dt, int64_t ld_out,
+                       hipStream_t st) {
   using namespace moe;
-  const I8GemmArgs g{a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
+  const I8GemmArgs g{plain, a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
                      out, out_dt, ld_out};
   // rows of a product and products: of the experts' rows only their sum is known here, so each is
   // taken to have the mean (padding included). The many rounds of I8Mid over many experts take 172

@@ -43,3 +43,12 @@ def test_products_refuse_matrices_of_2_gb_and_more(N, glu):
         assert L.i8_linear(FAKE, BF16, 64, rows, w, FAKE, FAKE, FAKE, BF16, INT_MAX, None) == ESHAPE
     assert L.i8_moe_gemm(FAKE, FAKE, FAKE, 8, w, FAKE, FAKE, 16, 64, 0, 1.702, 7.0, FAKE,
                          None) == ESHAPE
+
+
+@no_gpu
+def test_linear_refuses_a_product_too_large_for_a_launch_before_it_quantizes():
+    """The grid of a product has fewer than 2^32 threads. i8_linear says so as i8_gemm does, before
+    its quantizer is launched (which reports another status here: there is no device)."""
+    L, w = _lib.lib(), stack(N=1, K=1)
+    assert L.i8_gemm(FAKE, FAKE, INT_MAX, w, FAKE, BF16, 1, None) == ESHAPE
+    assert L.i8_linear(FAKE, BF16, 1, INT_MAX, w, FAKE, FAKE, FAKE, BF16, 1, None) == ESHAPE
