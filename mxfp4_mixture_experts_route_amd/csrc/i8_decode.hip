@@ -186,7 +186,8 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
                       uint16_t* __restrict__ h) {
   extern __shared__ __attribute__((aligned(16))) uint8_t rowsq[];   // part of the row per wavefront
   constexpr int kWaves = kI8DecThreads / kWave;
-  __shared__ uint64_t keys[kWaves][kWave];
+  __shared__ __attribute__((aligned(16))) uint64_t keys[kWaves][kWave];
+  static_assert(__alignof__(keys) >= 16, "wave_rank_keys reads the keys in pairs");
   __shared__ int red[kWaves][kI8TileRows];
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
