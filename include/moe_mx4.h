@@ -479,8 +479,10 @@ int i8_quantize(const void* x, int x_dtype, int64_t ld, const int32_t* live, int
 /*
  * Dense product of quantized rows with one matrix (w->E == 1):
  *   out[r][n] = (sum_i aq[r][i] * wq[n][i]) * (as[r] * s[n]) + bias[n]
- * the sum exact in 32-bit integers, the rest in fp32, rounded once to out_dtype. With glu = 1 the
- * channels come out in their order (gate rows, then up rows).
+ * the sum exact in 32-bit integers, the rest in fp32, rounded once to out_dtype; where as[r] * s[n]
+ * is no normal fp32 number the rest is computed in 64 bits (and rounded to fp32), so scales of any
+ * size are taken and a sum of zero gives the bias. With glu = 1 the channels come out in their order
+ * (gate rows, then up rows).
  *   out   out_dtype [rows][N], ld_out elements from one row to the next (ld_out >= N).
  * i8_linear: the same from plain rows x (as i8_quantize takes them); q_ws (int8 [rows][KP]) and
  * s_ws (f32 [rows]) are scratch that the call may write and leaves without meaning (a few

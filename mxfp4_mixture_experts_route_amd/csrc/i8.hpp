@@ -204,6 +204,35 @@ __device__ __forceinline__ uint2 codes8(const I8Quant& z, float (&v)[8]) {
   return o;
 }
 
+// Values of sums of products: sum * (sr * sc) + bias, with the scales of a row and of a channel, as
+// one f32 product and one fused multiply-add. Where the product of the scales is no normal f32 (zero,
+// subnormal: few or no bits left; infinite: a sum of zero would give NaN) the value may be an
+// ordinary number all the same: it is then computed in 64 bits, which hold the product of two f32
+// exactly, and rounded to f32. One branch covers the N values: such scales are rare.
+template <int N>
+__device__ __forceinline__ void i8_scaled(const int (&sum)[N], const float (&sr)[N], const float (&sc)[N],
+                                          const float (&bias)[N], float (&v)[N]) {
+  constexpr int kNormalOrNaN = 0x10B;   // v_cmp_class: NaN (1, 2), normal numbers (8, 0x100)
+  bool odd[N], any = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float p = sr[i] * sc[i];
+    odd[i] = !__builtin_amdgcn_classf(p, kNormalOrNaN);
+    any |= odd[i];
+    v[i] = fmaf((float)sum[i], p, bias[i]);
+  }
+  if (__builtin_expect(any, 0)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (odd[i]) v[i] = (float)fma((double)sum[i], (double)sr[i] * (double)sc[i], (double)bias[i]);
+  }
+}
+__device__ __forceinline__ float i8_scaled(int sum, float sr, float sc, float bias) {
+  float v[1];
+  i8_scaled<1>({sum}, {sr}, {sc}, {bias}, v);
+  return v[0];
+}
+
 // The clamped SwiGLU of a pair, NaN where either is NaN (the clamps alone would take a NaN to the
 // limit, and a row without a scale has to stay without a value).
 __device__ __forceinline__ float i8_swiglu(float gate, float up, float alpha, float limit) {

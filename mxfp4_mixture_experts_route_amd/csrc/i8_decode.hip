@@ -243,8 +243,8 @@ i8_one_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __restri
     for (int i = 0; i < 4; ++i) red[wave][4 * g + i] = acc[i];
   lds_barrier();
   if (tid < kI8TileRows && n < F) {
-    const float gate = fmaf((float)(red[0][tid] + red[1][tid]), z.s * sg, bg);
-    const float up = fmaf((float)(red[2][tid] + red[3][tid]), z.s * su, bu);
+    const float gate = i8_scaled(red[0][tid] + red[1][tid], z.s, sg, bg);
+    const float up = i8_scaled(red[2][tid] + red[3][tid], z.s, su, bu);
     h[(int64_t)j * F + n] = bf16_one(i8_swiglu(gate, up, alpha, limit));
   }
 }
@@ -300,7 +300,7 @@ i8_one_down_kernel(const uint16_t* __restrict__ h, int E, int k, int parts,
   if (part == 0 && lane < kI8TileRows) {
     int sum = 0;
     for (int p = 0; p < parts; ++p) sum += red[wave + p][lane];
-    const float dv = fmaf((float)sum, z.s * sc, bi);
+    const float dv = i8_scaled(sum, z.s, sc, bi);
     if (d && n < D) d[(int64_t)slot * D + n] = dv;
     dv_s[slot][lane] = wt;
     red[wave][lane] = __float_as_int(dv);
@@ -434,8 +434,8 @@ i8_decode_gate_up_kernel(const float* __restrict__ logits, const uint16_t* __res
     if (m < cnt && n < F) {
       const int from = (jj >> 2) * 16 + m, i = jj & 3;
       const float sa = sx[m];
-      const float gate = fmaf((float)(rd[0][from][i] + rd[1][from][i]), sa * sg, bg);
-      const float up = fmaf((float)(rd[2][from][i] + rd[3][from][i]), sa * su, bu);
+      const float gate = i8_scaled(rd[0][from][i] + rd[1][from][i], sa, sg, bg);
+      const float up = i8_scaled(rd[2][from][i] + rd[3][from][i], sa, su, bu);
       h[(int64_t)list[m] * F + n] = bf16_one(i8_swiglu(gate, up, alpha, limit));
     }
   }
@@ -542,7 +542,8 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
 #pragma unroll
   for (int i = 0; i < kSums; ++i) {
     const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
-    dsc[i] = dbi[i] = 0.0f;
+    dsc[i] = 1.0f;
+    dbi[i] = 0.0f;
     if (r < R && n < D) {
       const int64_t cg = (int64_t)sid[r] * D + n;
       dsc[i] = wsc[cg];
@@ -587,7 +588,7 @@ i8_decode_down_kernel(const uint16_t* __restrict__ h, const int8_t* __restrict__
   for (int i = 0; i < kSums; ++i) {
     const int r = (tid >> 4) + i * (kI8DownThreads / kI8TileRows);
     if (r >= R) break;
-    const float dv = fmaf((float)acc_s[r][jj], sh[r] * dsc[i], dbi[i]);
+    const float dv = i8_scaled(acc_s[r][jj], sh[r], dsc[i], dbi[i]);
     if (d && n < D) d[(int64_t)r * D + n] = dv;
     acc_s[r][jj] = __float_as_int(dv);
   }

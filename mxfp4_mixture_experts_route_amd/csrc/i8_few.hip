@@ -80,7 +80,7 @@ i8_few_kernel(const void* __restrict__ x, int64_t ld, int rows, const int8_t* __
     int sum = 0;
 #pragma unroll
     for (int p = 0; p < kWaves; ++p) sum += red[p][from][i];
-    store_elem(out, m * ld_out + n, fmaf((float)sum, sx[m] * sc, bi), out_dt);
+    store_elem(out, m * ld_out + n, i8_scaled(sum, sx[m], sc, bi), out_dt);
   }
 }
 

@@ -318,7 +318,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
 #pragma unroll
   for (int i = 0; i < kRowsT; ++i) {
     const int m = tid + i * TL::kThreads;
-    row_scale[i] = 0.0f;
+    row_scale[i] = 1.0f;   // (of what is not stored)
     if (m < BM && src_s[m] >= 0) row_scale[i] = as[src_s[m]];
   }
 #pragma unroll
@@ -326,7 +326,8 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     const int j = tid + i * TL::kThreads, u = j >> 4;   // SwiGLU: even tiles are gate, odd ones up
     const int t = GLU ? ((u & 1) ? HT : 0) + min(u0 + (u >> 1), HT - 1) : min(u0 + u, NT - 1);
     const int n = j < BN ? i8_channel(t, j & 15, N, glu) : -1;
-    ch_scale[i] = ch_bias[i] = 0.0f;
+    ch_scale[i] = 1.0f;
+    ch_bias[i] = 0.0f;
     if (n >= 0) {
       ch_scale[i] = wsc[(int64_t)e * N + n];
       if (bias) ch_bias[i] = bias[(int64_t)e * N + n];
@@ -492,18 +493,22 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
     const float4 sw = *reinterpret_cast<const float4*>(wsc_s + j);
     const float4 sb = *reinterpret_cast<const float4*>(bias_s + j);
     const i32x4_t t = quad(f, m, q);
-    float v[4] = {fmaf((float)t[0], sa * sw.x, sb.x), fmaf((float)t[1], sa * sw.y, sb.y),
-                  fmaf((float)t[2], sa * sw.z, sb.z), fmaf((float)t[3], sa * sw.w, sb.w)};
+    float v[4];
     int ch = j;
     if constexpr (GLU) {
       const float4 uw = *reinterpret_cast<const float4*>(wsc_s + j + 16);
       const float4 ub = *reinterpret_cast<const float4*>(bias_s + j + 16);
       const i32x4_t u = quad(f, m, q + 2);
-      v[0] = i8_swiglu(v[0], fmaf((float)u[0], sa * uw.x, ub.x), alpha, limit);
-      v[1] = i8_swiglu(v[1], fmaf((float)u[1], sa * uw.y, ub.y), alpha, limit);
-      v[2] = i8_swiglu(v[2], fmaf((float)u[2], sa * uw.z, ub.z), alpha, limit);
-      v[3] = i8_swiglu(v[3], fmaf((float)u[3], sa * uw.w, ub.w), alpha, limit);
+      float gu[8];
+      i8_scaled<8>({t[0], t[1], t[2], t[3], u[0], u[1], u[2], u[3]}, {sa, sa, sa, sa, sa, sa, sa, sa},
+                   {sw.x, sw.y, sw.z, sw.w, uw.x, uw.y, uw.z, uw.w},
+                   {sb.x, sb.y, sb.z, sb.w, ub.x, ub.y, ub.z, ub.w}, gu);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = i8_swiglu(gu[i], gu[i + 4], alpha, limit);
       ch = (wn * FN + f) * 16 + 8 * q + 4 * hi;
+    } else {
+      i8_scaled<4>({t[0], t[1], t[2], t[3]}, {sa, sa, sa, sa}, {sw.x, sw.y, sw.z, sw.w},
+                   {sb.x, sb.y, sb.z, sb.w}, v);
     }
     uint8_t* const dst = stage + lr * kPitch + ch * kSize;
     if constexpr (OUT == MOE_F32) {
