@@ -816,13 +816,17 @@ def moe_layer(x, logits, gate_up, down, k: int, tile_m: int,
     projection: "gemm" or "gemv" (bf16 activations), or "gemm_mx8" (MXFP8 activations on the
     MX-scaled MFMA: x quantized once, h written as MXFP8 rows by the gate_up epilogue; returns
     xq/xs/hq/hs and no bf16 h); these take MX4Experts. "i8" takes I8Experts (gate_up with glu):
-    x and h quantized per row (xq/xs/hq/hs are returned too).
+    x and h quantized per row (xq/xs/hq/hs are returned too), a stream argument covering
+    everything the call does, what it allocates included.
     Returns a dict of every intermediate (device tensors)."""
     if projection not in ("gemm", "gemv", "gemm_mx8", "i8"):
         raise ValueError(f"unknown projection {projection!r}")
     for name, stack in (("gate_up", gate_up), ("down", down)):
         if isinstance(stack, I8Experts) != (projection == "i8"):
             raise TypeError(f"{name}: {type(stack).__name__} in projection {projection!r}")
+    if projection == "i8" and stream is not None:   # routing and sums belong to the stream too
+        with _i8_on(stream, x):
+            return moe_layer(x, logits, gate_up, down, k, tile_m, alpha, limit, projection)
     T, E = logits.shape
     ids, w = moe_route_topk(logits, k, stream=stream)
     mpad = moe_mpad_max(T, k, E, tile_m)
