@@ -519,7 +519,9 @@ int i8_moe_gemm(const int8_t* aq, const float* as, const int32_t* a_row, int64_t
  * the third quantizes h, which launch 2 otherwise does on the way): what
  * moe_route_topk, i8_quantize, i8_moe_gemm with MOE_ACT_SWIGLU_OAI, i8_quantize,
  * i8_moe_gemm with MOE_ACT_NONE and moe_combine compute, bit for bit, with h and d by routed row
- * rho = t*k + s. An expert is read once however many of the tokens picked it.
+ * rho = t*k + s. An expert is read once however many of the tokens picked it. Made for D and F up to
+ * 4096 and E up to 128: past them it is right and slower, and for some ten tokens and more the
+ * single calls can be faster there.
  *   logits f32 [T][E];  x bf16 [T][D];  w_gu: glu = 1, N = 2F, K = D;  w_dn: glu = 0, N = D, K = F
  *   ids i32 [T][k], w f32 [T][k] out (as moe_route_topk);  h bf16 [T*k][F] out
  *   q_ws int8 [T*k][roundup(F, 128)], s_ws f32 [T*k]: scratch that the call may write and leaves

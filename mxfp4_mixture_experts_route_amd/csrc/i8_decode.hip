@@ -16,8 +16,12 @@
 // results are those of i8_quantize, i8_moe_gemm and moe_combine bit for bit.
 //
 // Bound by the stream of weights: 3 D F bytes of every picked expert. At D = F = 2880, k = 4: one
-// token 11.7 + 9.0 us (99.5 MB, 4.8 TB/s); 16 tokens of 32 experts 70 + 4 + 40 us (620 MB, 5.4 TB/s);
-// 5 tokens of 128 experts 48 + 4 + 27 us (470 MB, 6.0 TB/s).
+// token 11.7 + 9.6 us (99.5 MB, 4.7 TB/s); 16 tokens of 32 experts 71 + 5 + 38 us (620 MB, 5.4 TB/s);
+// 5 tokens of 128 experts 50 + 5 + 29 us (470 MB, 5.6 TB/s).
+// Rows of more than 4096 values do not fit the registers: they are read twice and the weights go out
+// behind them, and one token goes the way of several (32 experts, k = 4, D = F = 4096 and 4160, by the
+// rate of the weights: one token 5.1 and 3.3 TB/s, 5 tokens 5.6 and 4.8, 16 tokens 5.9 and 5.1).
+// More than 128 experts are routed by the slower wave_topk (5 tokens: 128 experts 86 us, 129 90).
 #include "i8.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"

@@ -3,7 +3,8 @@
 //
 // Bound by the stream of weights (N K bytes), and for small matrices by latency: the row is read,
 // its largest magnitude found and its codes formed while the first weights are on their way
-// (2880 -> 5760 channels, 16.6 MB: 6.5 us for one row, 7.2 for four, of which a launch is 4).
+// (2880 -> 5760 channels, 16.6 MB: 6.6 us for one row, 7.3 for four; the least there is to do, one
+// tile of 64 values, 3.3; a launch that does next to nothing 1.6. Calls captured into one graph.)
 // Products run on v_mfma_i32_16x16x64_i8 (a weight tile is A, the rows are columns of B); the sums
 // are exact 32-bit integers (K <= 65536 keeps 128 * 128 * K below 2^31), so the split of K changes
 // no result.

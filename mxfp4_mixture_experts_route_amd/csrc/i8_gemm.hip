@@ -20,9 +20,9 @@
 //    values and the 8 up values of the same channels.
 //
 // What bounds it: with few rows an expert the stream of weights (32 experts of 5760 x 2880, 64
-// tokens: 80 us, 6.7 TB/s); with more of them what a CU takes in, weights and activations, from L2
-// and beyond (512 tokens: 105 us, matrix cores busy 28 % of the time); in large dense products the
-// matrix cores (4096 rows, 8192 -> 8192: 253 us, 2.2 POPS).
+// tokens: 79 us, 6.8 TB/s); with more of them what a CU takes in, weights and activations, from L2
+// and beyond (512 tokens: 101 us, matrix cores busy 28 % of the time); in large dense products the
+// matrix cores (4096 rows, 8192 -> 8192: 248 to 256 us, 2.2 POPS, matrix cores busy 52 %).
 #include "i8.hpp"
 #include "launch.hpp"
 
@@ -180,7 +180,7 @@ i8_gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ as,
   nb = __builtin_amdgcn_readfirstlane(nb);
   int64_t count = ROUTED ? (int64_t)counts[e] : rows;
   const int64_t base = ROUTED ? (int64_t)basep[e] : 0;
-  count = min(count, mpad - base);   // never past the output, whatever the CSR holds
+  count = min(count, mpad - base);   // never past the output
   if (base < 0) return;
   const int64_t r0 = (int64_t)mb * BM;
   const int live = (int)min((int64_t)BM, count - r0);
@@ -685,11 +685,13 @@ int moe_launch_i8_gemm(const moe::I8Plain* plain, const int8_t* a, const float* 
   const I8GemmArgs g{plain, a, as, a_row, a_rows, w, counts, basep, rows, mpad, alpha, limit,
                      out, out_dt, ld_out};
   // rows of a product and products: of the experts' rows only their sum is known here, so each is
-  // taken to have the mean (padding included). The many rounds of I8Mid over many experts take 172
-  // ns each. gate_up of 32 experts, 64 tokens: I8Mid 79 us, I8Wide 88; 256 tokens: 89 and 96; 512
-  // tokens: 115 and 107; 2048 tokens: 228 and 195. 10 experts of 87 rows, 2338 -> 69 channels:
-  // I8Few 6.2 us, I8Wide 22.9; 6 of 3 rows, 1331 -> 1105: I8Few 5.4, I8Mid 12.3; 20 of 134 rows,
-  // 1982 -> 2 x 98: I8Half 10.8, I8Wide 19.8; 59 of 130 rows, 573 -> 326: I8Mid 14.2, I8Wide 19.7
+  // taken to have the mean, padding included: with much padding the tile is too tall (64 tokens of
+  // 32 experts: tile_m 16 87 us by I8Mid, tile_m 64 and 256 92 by I8Wide). The many rounds of I8Mid
+  // over many experts take 172 ns each. gate_up of 32 experts, 64 tokens: I8Mid 79 us, I8Wide 88;
+  // 256 tokens: 89 and 96; 512 tokens: 115 and 107; 2048 tokens: 228 and 195. 10 experts of 87
+  // rows, 2338 -> 69 channels: I8Few 6.2 us, I8Wide 22.9; 6 of 3 rows, 1331 -> 1105: I8Few 5.4,
+  // I8Mid 12.3; 20 of 134 rows, 1982 -> 2 x 98: I8Half 10.8, I8Wide 19.8; 59 of 130 rows, 573 ->
+  // 326: I8Mid 14.2, I8Wide 19.7
   const bool glu = act == MOE_ACT_SWIGLU_OAI;
   const int64_t n = counts ? (mpad + w->E - 1) / w->E : rows, E = counts ? w->E : 1;
   const int units = i8_tiles(w->N, w->glu);
